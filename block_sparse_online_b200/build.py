@@ -21,7 +21,7 @@ LIB = os.path.join(PKG, "libsolattn.so")
 # a failed check records SOLATTN_EBOUNDS in the workspace status word instead of touching
 # memory out of range. Same exports; load it explicitly (solattn.load_library(DEBUG_LIB)).
 DEBUG_LIB = os.path.join(PKG, "libsolattn_debug.so")
-SOURCES = ["solattn_api.cu"]
+SOURCES = ["solattn_api.cu", "dense_api.cu"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -34,7 +34,7 @@ def nvcc() -> str:
 
 def build(verbose: bool = False, extra=(), debug: bool = False) -> str:
     out = DEBUG_LIB if debug else LIB
-    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "-shared", "-Xcompiler", "-fPIC",
+    cmd = [nvcc(), *ARCH, "-O3", "-lineinfo", "-std=c++17", "--threads", str(len(SOURCES)), "-shared", "-Xcompiler", "-fPIC",
            "-I", INCLUDE, "-I", CSRC, "-o", out, *[os.path.join(CSRC, s) for s in SOURCES], *extra]
     if debug:
         cmd.insert(1, "-DSOLATTN_DEBUG")

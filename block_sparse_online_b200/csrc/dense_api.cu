@@ -1,0 +1,310 @@
+// dense_api.cu -- host side of the dense attention entry points and of the cache: argument
+// checks, choice of kernel, launches.
+#include <cuda.h>
+#include <cuda_runtime.h>
+
+#include <cmath>
+#include <cstdint>
+#include <type_traits>
+
+#include "cache_kernel.cuh"
+#include "dense_common.cuh"
+#include "host_common.h"
+#include "rows_kernel.cuh"
+#include "solattn.h"
+
+namespace {
+
+using namespace solattn;
+
+constexpr size_t kHeader = 256;  // [4]: status word
+constexpr unsigned long long kTimeoutNs = 2000000000ull;
+constexpr int kMaxSms = 160;     // blocks per SM slot that the workspace provides for
+constexpr int kRowsBlocks1 = 3 * kMaxSms, kRowsBlocks2 = 2 * kMaxSms;
+
+// Workspace: header, one record per block, then maxima and sums, then outputs of the parts.
+struct DenseWs {
+  size_t desc, ml, o, total;
+};
+DenseWs dense_ws(int d) {
+  // the larger of the kernels' needs: two parts per block
+  const size_t rows = 2 * static_cast<size_t>(kRowsBlocks2) * 16;
+  static_assert(kRowsBlocks1 * 8 <= kRowsBlocks2 * 16, "part rows");
+  DenseWs w;
+  w.desc = kHeader;
+  w.ml = w.desc + align_up(sizeof(int4) * kRowsBlocks1, kAlign);
+  w.o = w.ml + align_up(rows * 2 * sizeof(float), kAlign);
+  w.total = w.o + align_up(rows * d * sizeof(float), kAlign);
+  return w;
+}
+
+bool heads_ok(int H, int Hkv) { return H >= 1 && Hkv >= 1 && H % Hkv == 0; }
+
+// Strides of a view that the kernels can follow: 16-byte steps, and for an output no step of zero.
+bool view_ok(const solattn_view *x, int elem, bool output, int64_t nb, int64_t nh, int64_t nn) {
+  if (!x || !x->ptr || !aligned(x->ptr, 16)) return false;
+  const int64_t step = 16 / elem;
+  const int64_t st[3] = {x->stride_b, x->stride_h, x->stride_n};
+  const int64_t ext[3] = {nb, nh, nn};
+  for (int i = 0; i < 3; ++i) {
+    if (ext[i] <= 1) continue;
+    if (st[i] < 0 || st[i] % step != 0 || (output && st[i] == 0)) return false;
+  }
+  return true;
+}
+
+int check_device(std::initializer_list<const void *> ptrs, DeviceInfo *di) {
+  if (device_info(di) != SOLATTN_OK) return SOLATTN_ECUDA;
+  if (di->major != 10) return SOLATTN_EUNSUPPORTED;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return SOLATTN_ECUDA;
+  for (const void *p : ptrs)
+    if (p && foreign_device_pointer(p, dev)) return SOLATTN_EINVAL;
+  return SOLATTN_OK;
+}
+
+int check_cache(const solattn_cache *c) {
+  if (!c) return SOLATTN_EINVAL;
+  if (c->num_pages < 1 || c->Hkv < 1) return SOLATTN_EINVAL;
+  if (c->kind < SOLATTN_CACHE_16 || c->kind > SOLATTN_CACHE_E4M3) return SOLATTN_EINVAL;
+  if (c->d != 64 && c->d != 128) return SOLATTN_EUNSUPPORTED;
+  if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128) return SOLATTN_EUNSUPPORTED;
+  const int elem = c->kind == SOLATTN_CACHE_16 ? 2 : 1;
+  if (!view_ok(&c->k, elem, true, c->num_pages, c->Hkv, c->page) || !view_ok(&c->v, elem, true, c->num_pages, c->Hkv, c->page))
+    return SOLATTN_EINVAL;
+  if (c->kind != SOLATTN_CACHE_16 &&
+      (!c->k_scale || !c->v_scale || !aligned(c->k_scale, 4) || !aligned(c->v_scale, 4)))
+    return SOLATTN_EINVAL;
+  return SOLATTN_OK;
+}
+
+int check_seqs(const solattn_seqs *s, int page) {
+  if (!s || s->B < 1 || s->total < 0 || s->width < 1) return SOLATTN_EINVAL;
+  if (!s->table || !s->cu || !s->len) return SOLATTN_EINVAL;
+  if (!aligned(s->table, 4) || !aligned(s->cu, 4) || !aligned(s->len, 4)) return SOLATTN_EINVAL;
+  if (static_cast<long long>(s->width) * page > (1ll << 30)) return SOLATTN_EUNSUPPORTED;  // positions are 32-bit
+  return SOLATTN_OK;
+}
+
+int page_shift(int page) { return page == 16 ? 4 : page == 32 ? 5 : page == 64 ? 6 : 7; }
+
+// A launch that may begin while the launch before it ends (its kernel waits for the data).
+template <class K, class... Args>
+bool launch(K kernel, dim3 grid, dim3 block, cudaStream_t st, bool dependent, Args... args) {
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.stream = st;
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  cfg.attrs = &at;
+  cfg.numAttrs = dependent ? 1 : 0;
+  return cudaLaunchKernelEx(&cfg, kernel, args...) == cudaSuccess;
+}
+
+// Items of a call with at least 6 times as many as blocks are not split: the uneven share of the last
+// items costs less than the parts' traffic.
+constexpr int kWholeItems = 6;
+
+template <class QT, int KIND, int D, int NT, bool PAGED>
+int launch_rows(const DenseArgs &a, int sms, cudaStream_t st) {
+  using T = RowTiles<8 * NT>;
+  const int blocks = (NT == 1 ? 3 : 2) * sms;
+  // A block's share is at least two units (256 keys) when the items alone do not fill the launch.
+  if (!launch(rows_kernel<QT, KIND, D, NT, PAGED>, blocks, kRowsWarps * 32, st, false, a, 2, kWholeItems)) return SOLATTN_ECUDA;
+  if (!launch(join_kernel<T, QT, D, T::RT>, blocks, 256, st, true, a)) return SOLATTN_ECUDA;
+  return SOLATTN_OK;
+}
+
+template <class QT, int KIND, int D, bool PAGED>
+int dispatch_rows(const DenseArgs &a, int rows, int sms, cudaStream_t st) {
+  return rows <= 8 ? launch_rows<QT, KIND, D, 1, PAGED>(a, sms, st) : launch_rows<QT, KIND, D, 2, PAGED>(a, sms, st);
+}
+
+template <class QT, int D>
+int dispatch_kind(const DenseArgs &a, int kind, int rows, int sms, cudaStream_t st) {
+  if (!a.table) return dispatch_rows<QT, kKind16, D, false>(a, rows, sms, st);
+  if (kind == SOLATTN_CACHE_16) return dispatch_rows<QT, kKind16, D, true>(a, rows, sms, st);
+  if (kind == SOLATTN_CACHE_INT8) return dispatch_rows<QT, kKindInt8, D, true>(a, rows, sms, st);
+  return dispatch_rows<QT, kKindE4m3, D, true>(a, rows, sms, st);
+}
+
+int dispatch_dense(const DenseArgs &a, int d, int dtype, int kind, int rows, int sms, cudaStream_t st) {
+  if (dtype == SOLATTN_BF16)
+    return d == 128 ? dispatch_kind<__nv_bfloat16, 128>(a, kind, rows, sms, st) : dispatch_kind<__nv_bfloat16, 64>(a, kind, rows, sms, st);
+  return d == 128 ? dispatch_kind<__half, 128>(a, kind, rows, sms, st) : dispatch_kind<__half, 64>(a, kind, rows, sms, st);
+}
+
+void set_workspace(DenseArgs *a, void *workspace, int d) {
+  const DenseWs wl = dense_ws(d);
+  uint8_t *ws = static_cast<uint8_t *>(workspace);
+  a->status = reinterpret_cast<int *>(ws + 4);
+  a->desc = reinterpret_cast<int4 *>(ws + wl.desc);
+  a->part_ml = reinterpret_cast<float *>(ws + wl.ml);
+  a->part_o = reinterpret_cast<float *>(ws + wl.o);
+  a->timeout_ns = kTimeoutNs;
+  a->scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(d));
+}
+
+int check_cross(int B, int H, int Hkv, int Nq, int Nk, int d) {
+  if (B < 1 || Nq < 0 || Nk < 0 || !heads_ok(H, Hkv)) return SOLATTN_EINVAL;
+  if (d != 64 && d != 128) return SOLATTN_EUNSUPPORTED;
+  // row and key indices are 32-bit
+  if (static_cast<long long>(Nq) * (H / Hkv) > (1ll << 30) || Nk > (1 << 30) || static_cast<long long>(B) * H > (1ll << 30))
+    return SOLATTN_EUNSUPPORTED;
+  return SOLATTN_OK;
+}
+
+int check_paged(int B, int H, int Hkv, int total, int d) {
+  if (B < 1 || total < 0 || !heads_ok(H, Hkv)) return SOLATTN_EINVAL;
+  if (d != 64 && d != 128) return SOLATTN_EUNSUPPORTED;
+  if (static_cast<long long>(total) * (H / Hkv) > (1ll << 30) || static_cast<long long>(B) * H > (1ll << 30))
+    return SOLATTN_EUNSUPPORTED;
+  return SOLATTN_OK;
+}
+
+template <class QT, int KIND, int D>
+bool launch_cache(const CacheArgs &a, bool write, int blocks, cudaStream_t st) {
+  return write ? launch(cache_kernel<QT, KIND, D, true>, blocks, kCacheThreads, st, false, a)
+               : launch(cache_kernel<QT, KIND, D, false>, blocks, kCacheThreads, st, false, a);
+}
+template <class QT, int D>
+bool dispatch_cache(const CacheArgs &a, int kind, bool write, int blocks, cudaStream_t st) {
+  if (kind == SOLATTN_CACHE_16) return launch_cache<QT, kKind16, D>(a, write, blocks, st);
+  if (kind == SOLATTN_CACHE_INT8) return launch_cache<QT, kKindInt8, D>(a, write, blocks, st);
+  return launch_cache<QT, kKindE4m3, D>(a, write, blocks, st);
+}
+
+int cache_impl(const solattn_cache *cache, const solattn_view *nk, const solattn_view *nv, const solattn_seqs *s,
+               int dtype, void *status, void *stream, bool write) {
+  const int rc = check_cache(cache);
+  if (rc != SOLATTN_OK) return rc;
+  const int rs = check_seqs(s, cache->page);
+  if (rs != SOLATTN_OK) return rs;
+  if (dtype != SOLATTN_BF16 && dtype != SOLATTN_FP16) return SOLATTN_EINVAL;
+  if (static_cast<long long>(s->total) * cache->Hkv > (1ll << 30)) return SOLATTN_EUNSUPPORTED;
+  if (!status || !aligned(status, kAlign)) return SOLATTN_EWORKSPACE;
+  if (s->total == 0) return SOLATTN_OK;
+  if (!view_ok(nk, 2, !write, 1, cache->Hkv, s->total) || !view_ok(nv, 2, !write, 1, cache->Hkv, s->total)) return SOLATTN_EINVAL;
+  DeviceInfo di;
+  const int rd = check_device({cache->k.ptr, cache->v.ptr, cache->k_scale, cache->v_scale, nk->ptr, nv->ptr, s->table, s->cu,
+                               s->len, status}, &di);
+  if (rd != SOLATTN_OK) return rd;
+  CacheArgs a{};
+  a.k = cache->k.ptr, a.v = cache->v.ptr, a.k_scale = cache->k_scale, a.v_scale = cache->v_scale;
+  a.k_row = cache->k.stride_n, a.k_head = cache->k.stride_h, a.k_seq = cache->k.stride_b;
+  a.v_row = cache->v.stride_n, a.v_head = cache->v.stride_h, a.v_seq = cache->v.stride_b;
+  a.new_k = nk->ptr, a.new_v = nv->ptr;
+  a.nk_tok = nk->stride_n, a.nk_head = nk->stride_h, a.nv_tok = nv->stride_n, a.nv_head = nv->stride_h;
+  a.table = s->table, a.cu = s->cu, a.len = s->len;
+  a.width = s->width, a.page = cache->page, a.page_shift = page_shift(cache->page), a.num_pages = cache->num_pages;
+  a.B = s->B, a.Hkv = cache->Hkv, a.total = s->total;
+  a.status = reinterpret_cast<int *>(static_cast<uint8_t *>(status) + 4);
+  // Tokens of a block: as many as leave four blocks per SM, at most kCacheTokens.
+  const int want = 4 * di.sms;
+  int tokens = s->total / want;
+  tokens = tokens < 1 ? 1 : tokens > kCacheTokens ? kCacheTokens : tokens;
+  a.tokens = tokens;
+  const int blocks = (s->total + tokens - 1) / tokens;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  NvtxRange r(write ? "solattn cache append" : "solattn cache read");
+  bool ok;
+  if (dtype == SOLATTN_BF16)
+    ok = cache->d == 128 ? dispatch_cache<__nv_bfloat16, 128>(a, cache->kind, write, blocks, st)
+                         : dispatch_cache<__nv_bfloat16, 64>(a, cache->kind, write, blocks, st);
+  else
+    ok = cache->d == 128 ? dispatch_cache<__half, 128>(a, cache->kind, write, blocks, st)
+                         : dispatch_cache<__half, 64>(a, cache->kind, write, blocks, st);
+  return ok ? SOLATTN_OK : SOLATTN_ECUDA;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t solattn_cross_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d) {
+  return check_cross(B, H, Hkv, Nq, Nk, d) == SOLATTN_OK ? dense_ws(d).total : 0;
+}
+
+size_t solattn_paged_workspace_size(int B, int H, int Hkv, int total, int d) {
+  return check_paged(B, H, Hkv, total, d) == SOLATTN_OK ? dense_ws(d).total : 0;
+}
+
+int solattn_cross(const solattn_view *q, const solattn_view *k, const solattn_view *v, const solattn_view *out,
+                  const int32_t *key_len, int B, int H, int Hkv, int Nq, int Nk, int d, int dtype, void *workspace,
+                  size_t ws_bytes, void *stream) {
+  if (!q || !k || !v || !out) return SOLATTN_EINVAL;
+  const int rc = check_cross(B, H, Hkv, Nq, Nk, d);
+  if (rc != SOLATTN_OK) return rc;
+  if (dtype != SOLATTN_BF16 && dtype != SOLATTN_FP16) return SOLATTN_EINVAL;
+  if (key_len && !aligned(key_len, 4)) return SOLATTN_EINVAL;
+  if (Nq > 0 && (!view_ok(q, 2, false, B, H, Nq) || !view_ok(out, 2, true, B, H, Nq))) return SOLATTN_EINVAL;
+  if (Nk > 0 && (!view_ok(k, 2, false, B, Hkv, Nk) || !view_ok(v, 2, false, B, Hkv, Nk))) return SOLATTN_EINVAL;
+  if (!workspace || !aligned(workspace, kAlign) || ws_bytes < dense_ws(d).total) return SOLATTN_EWORKSPACE;
+  if (Nq == 0) return SOLATTN_OK;
+  DeviceInfo di;
+  const int rd = check_device({q->ptr, k->ptr, v->ptr, out->ptr, key_len, workspace}, &di);
+  if (rd != SOLATTN_OK) return rd;
+  DenseArgs a{};
+  a.q = q->ptr, a.q_tok = q->stride_n, a.q_head = q->stride_h, a.q_batch = q->stride_b;
+  a.out = out->ptr, a.o_tok = out->stride_n, a.o_head = out->stride_h, a.o_batch = out->stride_b;
+  a.k = k->ptr, a.k_row = k->stride_n, a.k_head = k->stride_h, a.k_seq = k->stride_b;
+  a.v = v->ptr, a.v_row = v->stride_n, a.v_head = v->stride_h, a.v_seq = v->stride_b;
+  a.len = key_len;
+  a.B = B, a.Hkv = Hkv, a.G = H / Hkv, a.n = Nq, a.total = Nq, a.Lmax = Nk;
+  set_workspace(&a, workspace, d);
+  NvtxRange r("solattn cross attention");
+  const long long rows = static_cast<long long>(Nq) * a.G;
+  return dispatch_dense(a, d, dtype, SOLATTN_CACHE_16, static_cast<int>(rows), di.sms < kMaxSms ? di.sms : kMaxSms,
+                        static_cast<cudaStream_t>(stream));
+}
+
+int solattn_paged_forward(const solattn_view *q, const solattn_view *out, const solattn_cache *cache,
+                          const solattn_seqs *seqs, int H, int max_new, int causal, int dtype, void *workspace,
+                          size_t ws_bytes, void *stream) {
+  if (!q || !out) return SOLATTN_EINVAL;
+  const int rc = check_cache(cache);
+  if (rc != SOLATTN_OK) return rc;
+  const int rs = check_seqs(seqs, cache->page);
+  if (rs != SOLATTN_OK) return rs;
+  const int rp = check_paged(seqs->B, H, cache->Hkv, seqs->total, cache->d);
+  if (rp != SOLATTN_OK) return rp;
+  if (dtype != SOLATTN_BF16 && dtype != SOLATTN_FP16) return SOLATTN_EINVAL;
+  if (max_new < 0 || (causal != 0 && causal != 1)) return SOLATTN_EINVAL;
+  const int d = cache->d;
+  if (!workspace || !aligned(workspace, kAlign) || ws_bytes < dense_ws(d).total) return SOLATTN_EWORKSPACE;
+  if (seqs->total == 0) return SOLATTN_OK;
+  if (!view_ok(q, 2, false, 1, H, seqs->total) || !view_ok(out, 2, true, 1, H, seqs->total)) return SOLATTN_EINVAL;
+  DeviceInfo di;
+  const int rd = check_device({q->ptr, out->ptr, cache->k.ptr, cache->v.ptr, cache->k_scale, cache->v_scale, seqs->table,
+                               seqs->cu, seqs->len, workspace}, &di);
+  if (rd != SOLATTN_OK) return rd;
+  DenseArgs a{};
+  a.q = q->ptr, a.q_tok = q->stride_n, a.q_head = q->stride_h;
+  a.out = out->ptr, a.o_tok = out->stride_n, a.o_head = out->stride_h;
+  a.k = cache->k.ptr, a.k_row = cache->k.stride_n, a.k_head = cache->k.stride_h, a.k_seq = cache->k.stride_b;
+  a.v = cache->v.ptr, a.v_row = cache->v.stride_n, a.v_head = cache->v.stride_h, a.v_seq = cache->v.stride_b;
+  a.k_scale = cache->k_scale, a.v_scale = cache->v_scale;
+  a.table = seqs->table, a.width = seqs->width, a.page = cache->page, a.page_shift = page_shift(cache->page);
+  a.num_pages = cache->num_pages;
+  a.cu = seqs->cu, a.len = seqs->len;
+  a.B = seqs->B, a.Hkv = cache->Hkv, a.G = H / cache->Hkv, a.n = 0, a.total = seqs->total;
+  a.Lmax = seqs->width * cache->page, a.causal = causal;
+  set_workspace(&a, workspace, d);
+  NvtxRange r("solattn paged attention");
+  const int n = max_new < seqs->total ? max_new : seqs->total;
+  return dispatch_dense(a, d, dtype, cache->kind, n * a.G, di.sms < kMaxSms ? di.sms : kMaxSms, static_cast<cudaStream_t>(stream));
+}
+
+int solattn_cache_append(const solattn_cache *cache, const solattn_view *new_k, const solattn_view *new_v,
+                         const solattn_seqs *seqs, int dtype, void *status, void *stream) {
+  return cache_impl(cache, new_k, new_v, seqs, dtype, status, stream, true);
+}
+
+int solattn_cache_read(const solattn_cache *cache, const solattn_seqs *seqs, const solattn_view *k_out,
+                       const solattn_view *v_out, int dtype, void *status, void *stream) {
+  return cache_impl(cache, k_out, v_out, seqs, dtype, status, stream, false);
+}
+
+}  // extern "C"

@@ -8,9 +8,8 @@
 #include <cstring>
 #include <mutex>
 
-#include <nvtx3/nvToolsExt.h>
-
 #include "attn_kernel.cuh"
+#include "host_common.h"
 #include "plan_kernel.cuh"
 #include "pool_kernel.cuh"
 #include "route_kernels.cuh"
@@ -20,24 +19,10 @@ namespace {
 
 using namespace solattn;
 
-constexpr size_t kAlign = 256;
 constexpr size_t kHeaderBytes = 256;  // [0]: work counter (u32), [4]: status word (i32), [8]: plan counter
 constexpr unsigned long long kDefaultTimeoutNs = 2000000000ull;  // 2 s per device-side wait
 
-size_t align_up(size_t x, size_t a) { return (x + a - 1) / a * a; }
-
 int nblocks(int N, int blk) { return (N + blk - 1) / blk; }
-
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
-
-// NVTX range around the host code that enqueues one stage ("solattn pool", "solattn route",
-// "solattn attention", ...), for timeline tools; without a tool attached it costs a few ns.
-struct NvtxRange {
-  explicit NvtxRange(const char *name) { nvtxRangePushA(name); }
-  ~NvtxRange() { nvtxRangePop(); }
-  NvtxRange(const NvtxRange &) = delete;
-  NvtxRange &operator=(const NvtxRange &) = delete;
-};
 
 struct WsLayout {
   size_t qbar, kbar, vbar, v16, cost, order, kmom, theta, kbar16, vbar16, corr, keep, total;
@@ -70,48 +55,6 @@ WsLayout ws_layout(int B, int H, int N, int d, int Bq, int Bk) {
   w.keep = w.corr + align_up(bh * nblocks(N, Bq) * (d + 4) * sizeof(float), kAlign);  // keep bits
   w.total = w.keep + align_up(bh * nblocks(N, Bq) * ((nblocks(N, Bk) + 31) / 32) * sizeof(uint32_t), kAlign);
   return w;
-}
-
-struct DeviceInfo {
-  int sms = 0;
-  int major = 0;
-  bool known = false;
-};
-
-std::mutex g_mu;
-DeviceInfo g_dev[64];
-
-int device_info(DeviceInfo *out) {
-  int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SOLATTN_ECUDA;
-  std::lock_guard<std::mutex> lk(g_mu);
-  if (!g_dev[dev].known) {
-    int sms = 0, major = 0;
-    if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SOLATTN_ECUDA;
-    if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return SOLATTN_ECUDA;
-    g_dev[dev].sms = sms;
-    g_dev[dev].major = major;
-    g_dev[dev].known = true;
-  }
-  *out = g_dev[dev];
-  return SOLATTN_OK;
-}
-
-typedef CUresult (*EncodeTiledFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                  const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                  CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiledFn encode_fn() {
-  static EncodeTiledFn fn = nullptr;
-  static std::once_flag once;
-  std::call_once(once, [] {
-    void *ptr = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    if (cudaGetDriverEntryPoint("cuTensorMapEncodeTiled", &ptr, cudaEnableDefault, &q) == cudaSuccess &&
-        q == cudaDriverEntryPointSuccess)
-      fn = reinterpret_cast<EncodeTiledFn>(ptr);
-  });
-  return fn;
 }
 
 // 3-D view (d, N, B*H) of a contiguous bf16 [B][H][N][d] tensor; boxes of 64 x rows x 1
@@ -272,18 +215,6 @@ int launch_threshold(int d, const float *qbar, const float *kbar, float *kmom, f
                      float beta, bool diag, cudaStream_t st) {
   return d == 64 ? launch_threshold_d<64>(qbar, kbar, kmom, theta, BH, nQB, nKB, beta, diag, st)
                  : launch_threshold_d<128>(qbar, kbar, kmom, theta, BH, nQB, nKB, beta, diag, st);
-}
-
-// A device pointer that belongs to another GPU than the current one (the kernels would
-// read or write it from the wrong device). Host, managed and unregistered pointers pass:
-// the alignment and null checks above cover them, and managed memory is reachable.
-bool foreign_device_pointer(const void *p, int dev) {
-  cudaPointerAttributes a;
-  if (cudaPointerGetAttributes(&a, p) != cudaSuccess) {
-    cudaGetLastError();  // clear the sticky-free error of an unknown pointer
-    return false;
-  }
-  return a.type == cudaMemoryTypeDevice && a.device != dev;
 }
 
 int items_total(int B, int H, int N) {
@@ -758,6 +689,7 @@ const char *solattn_strerror(int status) {
     case SOLATTN_ECUDA: return "CUDA error";
     case SOLATTN_ETIMEOUT: return "device-side wait timed out";
     case SOLATTN_EWORKSPACE: return "workspace missing, misaligned or too small";
+    case SOLATTN_ETABLE: return "sequence length or page number outside the call's buffers";
     case SOLATTN_EBOUNDS: return "device-side bounds check failed (debug build)";
     default: return "unknown status";
   }

@@ -28,6 +28,7 @@ SOLATTN_ECUDA = -3
 SOLATTN_ETIMEOUT = -4
 SOLATTN_EWORKSPACE = -5
 SOLATTN_EBOUNDS = -6
+SOLATTN_ETABLE = -7
 MAX_KEY_BLOCKS = 1024
 
 EXPORTS = ("solattn_workspace_size", "solattn_pool", "solattn_forward", "solattn_forward_events",
@@ -35,7 +36,10 @@ EXPORTS = ("solattn_workspace_size", "solattn_pool", "solattn_forward", "solattn
            "solattn_host_workspace_size", "solattn_forward_host", "solattn_watchdog_selftest",
            "solattn_selftest_exp2", "solattn_forward_noalloc", "solattn_forward_gaussian", "solattn_forward_ex",
            "solattn_route_keep", "solattn_proxy_map_bytes", "solattn_route_topk", "solattn_route_topp",
-           "solattn_strerror")
+           "solattn_cross_workspace_size", "solattn_cross", "solattn_paged_workspace_size", "solattn_paged_forward",
+           "solattn_cache_append", "solattn_cache_read", "solattn_strerror")
+DTYPES = {torch.bfloat16: 0, torch.float16: 1}  # solattn_dtype
+CACHE_KINDS = {torch.int8: 1, torch.float8_e4m3fn: 2}  # solattn_cache_kind of 8-bit pages (16-bit pages: 0)
 GAUSS_VARIANTS = {"exact": 0, "diag": 1}  # solattn_gauss_variant
 RULES = {"running_max": 0, "gauss_exact": 1, "gauss_diag": 2}  # solattn_rule
 CORRECTIONS = {"block": 0, "token": 1}  # solattn_correction
@@ -54,6 +58,22 @@ class _Stats(ctypes.Structure):
 class _Route(ctypes.Structure):  # solattn_route
     _fields_ = [("rule", ctypes.c_int), ("tau", ctypes.c_float), ("beta", ctypes.c_float), ("n_sink", ctypes.c_int),
                 ("correction", ctypes.c_int)]
+
+
+class _View(ctypes.Structure):  # solattn_view
+    _fields_ = [("ptr", ctypes.c_void_p), ("stride_b", ctypes.c_int64), ("stride_h", ctypes.c_int64),
+                ("stride_n", ctypes.c_int64)]
+
+
+class _Cache(ctypes.Structure):  # solattn_cache
+    _fields_ = [("k", _View), ("v", _View), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int), ("Hkv", ctypes.c_int), ("page", ctypes.c_int), ("d", ctypes.c_int),
+                ("kind", ctypes.c_int)]
+
+
+class _Seqs(ctypes.Structure):  # solattn_seqs
+    _fields_ = [("table", ctypes.c_void_p), ("cu", ctypes.c_void_p), ("len", ctypes.c_void_p), ("B", ctypes.c_int),
+                ("width", ctypes.c_int), ("total", ctypes.c_int)]
 
 
 def _load(path=_LIB_PATH):
@@ -96,6 +116,19 @@ def _load(path=_LIB_PATH):
     lib.solattn_route_topk.restype = i
     lib.solattn_route_topp.argtypes = [vp, vp, i, i, i, i, i, i, f, vp, sz, vp, vp]
     lib.solattn_route_topp.restype = i
+    pv, pc, ps = ctypes.POINTER(_View), ctypes.POINTER(_Cache), ctypes.POINTER(_Seqs)
+    lib.solattn_cross_workspace_size.argtypes = [i, i, i, i, i, i]
+    lib.solattn_cross_workspace_size.restype = sz
+    lib.solattn_cross.argtypes = [pv, pv, pv, pv, vp, i, i, i, i, i, i, i, vp, sz, vp]
+    lib.solattn_cross.restype = i
+    lib.solattn_paged_workspace_size.argtypes = [i, i, i, i, i]
+    lib.solattn_paged_workspace_size.restype = sz
+    lib.solattn_paged_forward.argtypes = [pv, pv, pc, ps, i, i, i, i, vp, sz, vp]
+    lib.solattn_paged_forward.restype = i
+    lib.solattn_cache_append.argtypes = [pc, pv, pv, ps, i, vp, vp]
+    lib.solattn_cache_append.restype = i
+    lib.solattn_cache_read.argtypes = [pc, ps, pv, pv, i, vp, vp]
+    lib.solattn_cache_read.restype = i
     lib.solattn_strerror.argtypes = [i]
     lib.solattn_strerror.restype = ctypes.c_char_p
     return lib
@@ -459,4 +492,214 @@ def solattn_selftest_exp2(x: torch.Tensor, stream=None) -> torch.Tensor:
     return y
 
 
-__all__ = [n for n in globals() if n.startswith("solattn_")] + ["SolAttnError", "MODES"]
+# ---------------------------------------------------------------- dense attention and the cache
+
+
+def _rows(x, name, dtypes, shape, device):
+    """A strided tensor of rows of d contiguous elements; returns its type."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if x.dtype not in dtypes:
+        raise ValueError(f"{name} must have dtype {' or '.join(str(d) for d in dtypes)}, not {x.dtype}")
+    if not x.is_cuda or (device is not None and x.device != device):
+        raise ValueError(f"{name} is on {x.device}, " + (f"the inputs on {device}" if device else "not on a CUDA device"))
+    if tuple(x.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(x.shape)}, {tuple(shape)} expected")
+    if x.numel() and x.stride(-1) != 1:
+        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _view4(x):  # [B, heads, n, d]
+    st = x.stride()
+    return _View(x.data_ptr() or None, st[0], st[1], st[2])
+
+
+def _view3(x):  # packed rows [n, heads, d]
+    st = x.stride()
+    return _View(x.data_ptr() or None, 0, st[1], st[0])
+
+
+def _workspace(workspace, need, device):
+    """The caller's workspace, or a new one with its header cleared."""
+    if workspace is None:
+        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace[:256].zero_()
+        return workspace
+    _check_buffer(workspace, "workspace", (torch.uint8, torch.int8), need, device)
+    return workspace
+
+
+def alloc_status(device="cuda") -> torch.Tensor:
+    """A cleared status word (256 bytes) for :func:`solattn_cache_append` and :func:`solattn_cache_read`;
+    read it with :func:`solattn_get_status`."""
+    return torch.zeros(256, dtype=torch.uint8, device=device)
+
+
+def solattn_cross_workspace_size(B, H, Hkv, Nq, Nk, d) -> int:
+    return int(_lib.solattn_cross_workspace_size(B, H, Hkv, Nq, Nk, d))
+
+
+def solattn_paged_workspace_size(B, H, Hkv, total, d) -> int:
+    return int(_lib.solattn_paged_workspace_size(B, H, Hkv, total, d))
+
+
+def alloc_cross_workspace(B, H, Hkv, Nq, Nk, d, device="cuda") -> torch.Tensor:
+    """Workspace of :func:`solattn_cross`, its status word cleared."""
+    n = solattn_cross_workspace_size(B, H, Hkv, Nq, Nk, d)
+    if n == 0:
+        raise SolAttnError(SOLATTN_EUNSUPPORTED, "solattn_cross_workspace_size")
+    return _workspace(None, n, device)
+
+
+def solattn_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_len: torch.Tensor | None = None,
+                  out: torch.Tensor | None = None, workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Softmax attention of q [B, H, Nq, d] to keys and values [B, Hkv, Nk, d] of another length
+    (an encoder's states), bf16 or fp16, strided views allowed (rows contiguous).
+
+    ``key_len``: int32 [B] on the device, the keys of each sequence (the rest is padding that
+    may hold anything); a sequence of none gives zeros. H is a multiple of Hkv: query head h
+    uses key head h // (H // Hkv). Returns out [B, H, Nq, d]. Asynchronous on ``stream``;
+    lengths outside [0, Nk] are reported by :func:`solattn_get_status` on the workspace."""
+    B, H, Nq, d = _bhnd(q)
+    Hkv, Nk = (int(k.shape[1]), int(k.shape[2])) if isinstance(k, torch.Tensor) and k.dim() == 4 else (0, 0)
+    if q.dtype not in DTYPES:
+        raise ValueError(f"q must be bfloat16 or float16, not {q.dtype}")
+    dev, one = q.device, (q.dtype,)
+    _rows(q, "q", one, (B, H, Nq, d), None)
+    _rows(k, "k", one, (B, Hkv, Nk, d), dev)
+    _rows(v, "v", one, (B, Hkv, Nk, d), dev)
+    if out is None:
+        out = torch.empty_like(q) if 0 not in q.stride() else torch.empty((B, H, Nq, d), dtype=q.dtype, device=dev)
+    _rows(out, "out", one, (B, H, Nq, d), dev)
+    if key_len is not None:
+        _check_buffer(key_len, "key_len", (torch.int32,), B, dev)
+    need = solattn_cross_workspace_size(B, H, Hkv, Nq, Nk, d)
+    if need == 0:
+        raise SolAttnError(SOLATTN_EUNSUPPORTED, "solattn_cross")
+    workspace = _workspace(workspace, need, dev)
+    with torch.cuda.device(dev):
+        rc = _lib.solattn_cross(_view4(q), _view4(k), _view4(v), _view4(out),
+                                key_len.data_ptr() if key_len is not None else None, B, H, Hkv, Nq, Nk, d,
+                                DTYPES[q.dtype], workspace.data_ptr(), workspace.numel(), _stream(stream, dev))
+    _check(rc, "solattn_cross")
+    return out
+
+
+class PagedCache:
+    """A key/value cache in pages: k_pages and v_pages [num_pages, Hkv, page, d] in bf16 or fp16,
+    or as int8 or e4m3 codes with k_scale and v_scale fp32 [num_pages, Hkv, page], one
+    scale for each row. page is 16, 32, 64 or 128 tokens. The cache keeps references to the
+    tensors, not copies. A table [B, width] int32 names each sequence's pages in order
+    (entries behind its last page are not read)."""
+
+    def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor | None = None,
+                 v_scale: torch.Tensor | None = None):
+        P, Hkv, page, d = _bhnd(k_pages)
+        dt = k_pages.dtype
+        if dt not in DTYPES and dt not in CACHE_KINDS:
+            raise ValueError(f"pages must be bfloat16, float16, int8 or float8_e4m3fn, not {dt}")
+        _rows(k_pages, "k_pages", (dt,), (P, Hkv, page, d), None)
+        _rows(v_pages, "v_pages", (dt,), (P, Hkv, page, d), k_pages.device)
+        if (dt in CACHE_KINDS) != (k_scale is not None) or (dt in CACHE_KINDS) != (v_scale is not None):
+            raise ValueError("8-bit pages need k_scale and v_scale, 16-bit pages take none")
+        for name, sc in (("k_scale", k_scale), ("v_scale", v_scale)):
+            if sc is not None:
+                _check_buffer(sc, name, (torch.float32,), P * Hkv * page, k_pages.device)
+                if tuple(sc.shape) != (P, Hkv, page):
+                    raise ValueError(f"{name} has shape {tuple(sc.shape)}, {(P, Hkv, page)} expected")
+        self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
+        self.num_pages, self.Hkv, self.page, self.d, self.dtype, self.device = P, Hkv, page, d, dt, k_pages.device
+        self._c = _Cache(_view4(k_pages), _view4(v_pages), None if k_scale is None else k_scale.data_ptr(),
+                         None if v_scale is None else v_scale.data_ptr(), P, Hkv, page, d, CACHE_KINDS.get(dt, 0))
+
+    def _seqs(self, table, cu, length, total):
+        """The sequences of a call, checked."""
+        if not isinstance(table, torch.Tensor) or table.dim() != 2:
+            raise ValueError("table must be an int32 [B, width] tensor")
+        B, width = int(table.shape[0]), int(table.shape[1])
+        _check_buffer(table, "table", (torch.int32,), max(1, B * width), self.device)
+        _check_buffer(cu, "cu", (torch.int32,), B + 1, self.device)
+        _check_buffer(length, "length", (torch.int32,), B, self.device)
+        return _Seqs(table.data_ptr(), cu.data_ptr(), length.data_ptr(), B, width, total)
+
+    def _check_rows(self, x, name, total, dtype):
+        if dtype not in DTYPES or (self.dtype in DTYPES and dtype != self.dtype):
+            raise ValueError(f"{name} must be " + (str(self.dtype) if self.dtype in DTYPES else "bfloat16 or float16"))
+        _rows(x, name, (dtype,), (total, self.Hkv, self.d), self.device)
+
+
+def alloc_paged_workspace(cache: PagedCache, B, H, total, device=None) -> torch.Tensor:
+    """Workspace of :func:`solattn_paged_forward`, its status word cleared."""
+    n = solattn_paged_workspace_size(B, H, cache.Hkv, total, cache.d)
+    if n == 0:
+        raise SolAttnError(SOLATTN_EUNSUPPORTED, "solattn_paged_workspace_size")
+    return _workspace(None, n, cache.device if device is None else device)
+
+
+def solattn_paged_forward(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, cu: torch.Tensor,
+                          length: torch.Tensor, max_new: int, causal: bool = True, out: torch.Tensor | None = None,
+                          workspace: torch.Tensor | None = None, stream=None) -> torch.Tensor:
+    """Softmax attention of a batch's new tokens over a paged cache that already holds them.
+
+    q [total, H, d] (bf16 or fp16) packs the new tokens: rows cu[b] .. cu[b+1] - 1 are the last
+    ones of sequence b, which has length[b] tokens in the cache (table, cu, length: int32 on the
+    device). ``causal``: each sees the keys up to its own position; else the whole sequence.
+    ``max_new``: the most new tokens of a sequence, as far as the caller knows (it selects the
+    kernel, not the result). Rows behind cu[B] are left alone. Returns out [total, H, d].
+    Lengths or pages out of range are reported by :func:`solattn_get_status` on the workspace."""
+    if not isinstance(q, torch.Tensor) or q.dim() != 3:
+        raise ValueError("q must be a [total, H, d] tensor")
+    total, H = int(q.shape[0]), int(q.shape[1])
+    if q.dtype not in DTYPES or (cache.dtype in DTYPES and q.dtype != cache.dtype):
+        raise ValueError("q must be " + (str(cache.dtype) if cache.dtype in DTYPES else "bfloat16 or float16"))
+    dev = cache.device
+    _rows(q, "q", (q.dtype,), (total, H, cache.d), dev)
+    if out is None:
+        out = torch.empty((total, H, cache.d), dtype=q.dtype, device=dev)
+    _rows(out, "out", (q.dtype,), (total, H, cache.d), dev)
+    seqs = cache._seqs(table, cu, length, total)
+    need = solattn_paged_workspace_size(seqs.B, H, cache.Hkv, total, cache.d)
+    if need == 0:
+        raise SolAttnError(SOLATTN_EUNSUPPORTED, "solattn_paged_forward")
+    workspace = _workspace(workspace, need, dev)
+    with torch.cuda.device(dev):
+        rc = _lib.solattn_paged_forward(_view3(q), _view3(out), cache._c, seqs, H, int(max_new), int(bool(causal)),
+                                        DTYPES[q.dtype], workspace.data_ptr(), workspace.numel(), _stream(stream, dev))
+    _check(rc, "solattn_paged_forward")
+    return out
+
+
+def solattn_cache_append(cache: PagedCache, new_k: torch.Tensor, new_v: torch.Tensor, table: torch.Tensor,
+                         cu: torch.Tensor, length: torch.Tensor, workspace: torch.Tensor | None = None, stream=None):
+    """Writes the new tokens' keys and values [total, Hkv, d] (bf16 or fp16) into their pages,
+    quantised where the cache is 8-bit: scale = max|x| / TOP, code = nearest(x TOP / max|x|), TOP = 127
+    (int8) or 448 (e4m3). table, cu, length as in :func:`solattn_paged_forward` (length counts
+    the new tokens). ``workspace``: an :func:`alloc_status` tensor or any workspace."""
+    total = int(new_k.shape[0]) if isinstance(new_k, torch.Tensor) and new_k.dim() == 3 else -1
+    cache._check_rows(new_k, "new_k", total, getattr(new_k, "dtype", None))
+    cache._check_rows(new_v, "new_v", total, new_k.dtype)
+    seqs = cache._seqs(table, cu, length, total)
+    workspace = _workspace(workspace, 256, cache.device)
+    with torch.cuda.device(cache.device):
+        rc = _lib.solattn_cache_append(cache._c, _view3(new_k), _view3(new_v), seqs, DTYPES[new_k.dtype],
+                                       workspace.data_ptr(), _stream(stream, cache.device))
+    _check(rc, "solattn_cache_append")
+
+
+def solattn_cache_read(cache: PagedCache, table: torch.Tensor, cu: torch.Tensor, length: torch.Tensor,
+                       k_out: torch.Tensor, v_out: torch.Tensor, workspace: torch.Tensor | None = None, stream=None):
+    """Reads the new tokens' rows (the last cu[b+1] - cu[b] of each sequence) back from the pages into
+    k_out and v_out [total, Hkv, d] (bf16 or fp16): code * scale, rounded once. Returns them."""
+    total = int(k_out.shape[0]) if isinstance(k_out, torch.Tensor) and k_out.dim() == 3 else -1
+    cache._check_rows(k_out, "k_out", total, getattr(k_out, "dtype", None))
+    cache._check_rows(v_out, "v_out", total, k_out.dtype)
+    seqs = cache._seqs(table, cu, length, total)
+    workspace = _workspace(workspace, 256, cache.device)
+    with torch.cuda.device(cache.device):
+        rc = _lib.solattn_cache_read(cache._c, seqs, _view3(k_out), _view3(v_out), DTYPES[k_out.dtype],
+                                     workspace.data_ptr(), _stream(stream, cache.device))
+    _check(rc, "solattn_cache_read")
+    return k_out, v_out
+
+
+__all__ = [n for n in globals() if n.startswith("solattn_")] + ["PagedCache"] + ["SolAttnError", "MODES"]

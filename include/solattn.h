@@ -70,8 +70,10 @@ typedef enum {
   SOLATTN_ECUDA = -3,        /* a CUDA runtime or driver call failed                          */
   SOLATTN_ETIMEOUT = -4,     /* a device-side wait ran past its limit (reported by get_status) */
   SOLATTN_EWORKSPACE = -5,   /* workspace pointer null/misaligned or smaller than required     */
-  SOLATTN_EBOUNDS = -6       /* a device-side bounds check failed (libsolattn_debug.so only:
+  SOLATTN_EBOUNDS = -6,      /* a device-side bounds check failed (libsolattn_debug.so only:
                                 the build with -DSOLATTN_DEBUG; reported by get_status)        */
+  SOLATTN_ETABLE = -7        /* a sequence length or page number on the device lies outside the
+                                call's buffers (reported by get_status)                        */
 } solattn_status;
 
 /* Per-call statistics (device pointers). */
@@ -352,6 +354,115 @@ int solattn_watchdog_selftest(void *workspace, size_t ws_bytes, uint64_t limit_n
  * for x >= -125; smaller inputs are clamped to -125).
  */
 int solattn_selftest_exp2(const float *x, float *y, int n, void *stream);
+
+/*
+ * ---------------------------------------------------------------------------------------
+ * Dense attention beside the operator: to an encoder's states, and over a paged cache.
+ *
+ * A diffusion transformer's block attends its own tokens (solattn_forward) and, with the
+ * same heads, the states of a text or image encoder; a streaming generator attends a cache
+ * of earlier frames. These entry points compute plain softmax attention (no routing)
+ * for those two, in bf16 or fp16, with shared key heads and strided tensors, and write and
+ * read the cache, in 16 bits or quantised to 8. They are inference operators, as the rest
+ * of the library: no gradients.
+ *
+ * Common to all of them:
+ *   dtype      solattn_dtype of the 16-bit tensors
+ *   H, Hkv     query heads and key heads; Hkv divides H, query head h uses key head h / (H/Hkv)
+ *   d          64 or 128; the logits are scaled by 1/sqrt(d)
+ *   strides    in elements; the d elements of a row are contiguous, every stride is a
+ *              multiple of 8 elements (16 for 8-bit pages) and every base address of 16 bytes.
+ *              Inputs may overlap or repeat (stride 0); outputs may not
+ *   empty rows a query that sees no key gives a row of zeros
+ *   masked     keys and values behind a sequence's length are not used, whatever they hold.
+ *              Keys that only LATER queries see (causal) must have finite values (v)
+ *   lengths    cu and len are device data and unknown to the host. Values outside the
+ *              buffers are cut to them and page numbers outside the cache read as zeros (writes are
+ *              dropped); either is recorded as SOLATTN_ETABLE in the workspace's status word
+ *   workspace  device, 256-byte aligned, of the size that the size function gives; its first 256 bytes must be
+ *              zero before its first use. The status word keeps the first error until the
+ *              caller clears it. Not to be used by two calls that may run at the same time
+ *   errors     as solattn_forward; nothing is queued on an error
+ * ---------------------------------------------------------------------------------------
+ */
+typedef enum {
+  SOLATTN_BF16 = 0,
+  SOLATTN_FP16 = 1
+} solattn_dtype;
+
+/* A [B][heads][n][d] tensor. A tensor of packed rows [n][heads][d] has stride_b = 0. */
+typedef struct {
+  void *ptr;
+  int64_t stride_b, stride_h, stride_n;
+} solattn_view;
+
+/* What the pages of a cache hold. */
+typedef enum {
+  SOLATTN_CACHE_16 = 0,    /* rows in the calls' 16-bit dtype                                */
+  SOLATTN_CACHE_INT8 = 1,  /* int8 codes, one fp32 scale for each row of d: x = code * scale */
+  SOLATTN_CACHE_E4M3 = 2   /* the same with e4m3 codes                                       */
+} solattn_cache_kind;
+
+/*
+ * A cache: k and v are [num_pages][Hkv][page][d] views (stride_b of a page, stride_h of a
+ * head in it, stride_n of a row), k_scale and v_scale contiguous fp32 [num_pages][Hkv][page]
+ * (8-bit kinds only). page is 16, 32, 64 or 128 tokens.
+ */
+typedef struct {
+  solattn_view k, v;
+  float *k_scale, *v_scale;
+  int num_pages, Hkv, page, d, kind;
+} solattn_cache;
+
+/*
+ * The sequences of a call over a cache. Sequence b has len[b] tokens in the cache; position
+ * j of it is row j % page of page table[b * width + j / page]. Its NEW tokens, the last
+ * n_b = cu[b+1] - cu[b] of them, are rows cu[b] .. cu[b+1] - 1 of the packed tensors.
+ * Table entries behind a sequence's last page are not read. Two sequences may share pages
+ * that no call writes.
+ */
+typedef struct {
+  const int32_t *table; /* device [B][width]                                                  */
+  const int32_t *cu;    /* device [B+1], ascending from 0, at most total                      */
+  const int32_t *len;   /* device [B], n_b <= len[b] <= width * page                          */
+  int B, width, total;  /* total: rows of the packed tensors (those behind cu[B] are left alone) */
+} solattn_seqs;
+
+/*
+ * Attention of q [B][H][Nq][d] to k, v [B][Hkv][Nk][d]: sequence b's queries see its first
+ * key_len[b] keys (device int32 [B], or NULL: all Nk). Nq and Nk may be 0 or more.
+ */
+size_t solattn_cross_workspace_size(int B, int H, int Hkv, int Nq, int Nk, int d);
+int solattn_cross(const solattn_view *q, const solattn_view *k, const solattn_view *v, const solattn_view *out,
+                  const int32_t *key_len, int B, int H, int Hkv, int Nq, int Nk, int d, int dtype,
+                  void *workspace, size_t ws_bytes, void *stream);
+
+/*
+ * Attention of the new tokens q [total][H][d] (packed; stride_b ignored) over the cache,
+ * which already holds them. causal = 0: every new token sees its whole sequence; 1: up to its own position.
+ * max_new: the largest n_b the caller expects; it chooses the kernel only, and a larger n_b
+ * is computed all the same.
+ */
+size_t solattn_paged_workspace_size(int B, int H, int Hkv, int total, int d);
+int solattn_paged_forward(const solattn_view *q, const solattn_view *out, const solattn_cache *cache,
+                          const solattn_seqs *seqs, int H, int max_new, int causal, int dtype, void *workspace,
+                          size_t ws_bytes, void *stream);
+
+/*
+ * Writes the new tokens' keys and values [total][Hkv][d] into their pages. 8-bit kinds:
+ * scale = fl(max|x| / TOP) and code = nearest(x TOP / max|x|), ties to even, TOP = 127
+ * (int8) or 448 (e4m3); a row of zeros has scale 0, a row with an infinity or NaN has scale
+ * NaN. Two new tokens that share a page's row (pages shared by two sequences) are written in
+ * no particular order. status: device, 256-byte aligned, 256 bytes, zero before first use
+ * (any workspace of the calls above serves).
+ */
+int solattn_cache_append(const solattn_cache *cache, const solattn_view *new_k, const solattn_view *new_v,
+                         const solattn_seqs *seqs, int dtype, void *status, void *stream);
+
+/* Reads the new tokens' rows back into k_out and v_out [total][Hkv][d]: code * scale, rounded
+ * once. Rows whose page is outside the cache are left as they were. */
+int solattn_cache_read(const solattn_cache *cache, const solattn_seqs *seqs, const solattn_view *k_out,
+                       const solattn_view *v_out, int dtype, void *status, void *stream);
 
 /* Static description of a status code. */
 const char *solattn_strerror(int status);
