@@ -12,6 +12,7 @@
 #include "host_common.h"
 #include "rows_kernel.cuh"
 #include "solattn.h"
+#include "tile_kernel.cuh"
 
 namespace {
 
@@ -28,8 +29,8 @@ struct DenseWs {
 };
 DenseWs dense_ws(int d) {
   // the larger of the kernels' needs: two parts per block
-  const size_t rows = 2 * static_cast<size_t>(kRowsBlocks2) * 16;
-  static_assert(kRowsBlocks1 * 8 <= kRowsBlocks2 * 16, "part rows");
+  const size_t rows = 2 * static_cast<size_t>(kMaxSms) * TokenTiles::RT;
+  static_assert(kRowsBlocks1 * 8 <= kMaxSms * TokenTiles::RT && kRowsBlocks2 * 16 <= kMaxSms * TokenTiles::RT, "part rows");
   DenseWs w;
   w.desc = kHeader;
   w.ml = w.desc + align_up(sizeof(int4) * kRowsBlocks1, kAlign);
@@ -117,23 +118,109 @@ int launch_rows(const DenseArgs &a, int sms, cudaStream_t st) {
   return SOLATTN_OK;
 }
 
+// 16-bit tensor maps. Queries: (d, head of the group, token, key head, batch), boxes of 64 x G x tokens of
+// a half. Keys and values: (d, row, head, batch or page), boxes of 64 x rows. A dimension of stride zero has
+// extent one. Everything outside reads as zeros.
+int encode(CUtensorMap *map, int dtype, int rank, const void *ptr, const cuuint64_t *dims, const long long *strides, const cuuint32_t *box) {
+  EncodeTiledFn enc = encode_fn();
+  if (!enc) return SOLATTN_ECUDA;
+  cuuint64_t dm[5], st[4];
+  cuuint32_t one[5] = {1, 1, 1, 1, 1};
+  for (int i = 0; i < rank; ++i) dm[i] = dims[i];
+  for (int i = 1; i < rank; ++i) {
+    if (dm[i] > 1 && strides[i] == 0) dm[i] = 1;
+    st[i - 1] = dm[i] > 1 ? static_cast<cuuint64_t>(strides[i]) * 2 : 16;
+  }
+  const CUresult r = enc(map, dtype == SOLATTN_BF16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, rank,
+                         const_cast<void *>(ptr), dm, st, box, one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                         CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  return r == CUDA_SUCCESS ? SOLATTN_OK : SOLATTN_ECUDA;
+}
+
+// Whether the tile kernel can take the call: its copies need a token step in Q, K and V that is not
+// zero, strides below 2^40 bytes, and a group of heads that fits half a tile.
+bool tile_fits(const DenseArgs &a, int kind) {
+  if (a.G > 128 || a.Lmax == 0) return false;
+  if (kind != SOLATTN_CACHE_16) return true;  // no tensor maps
+  const long long most = 1ll << 39;
+  const long long st[] = {a.q_tok, a.q_head * a.G, a.q_batch, a.k_row, a.k_head, a.k_seq, a.v_row, a.v_head, a.v_seq};
+  for (long long x : st)
+    if (x >= most) return false;
+  if (a.q_tok == 0 && (a.cu ? a.total : a.n) > 1) return false;
+  if (a.q_head == 0 && a.G * a.Hkv > 1) return false;
+  if (!a.cu && a.q_batch == 0 && a.B > 1) return false;
+  if (!a.table && a.Lmax > 1 && (a.k_row == 0 || a.v_row == 0)) return false;
+  return true;
+}
+
 template <class QT, int KIND, int D, bool PAGED>
-int dispatch_rows(const DenseArgs &a, int rows, int sms, cudaStream_t st) {
+int launch_tiles(DenseArgs a, int dtype, int sms, cudaStream_t st) {
+  using C = TileCfg<QT, KIND, D, PAGED>;
+  constexpr size_t smem = tile_smem_bytes<C>();
+  static_assert(smem <= 232448, "shared memory");
+  auto kern = tile_kernel<C>;
+  static bool attr_set[64] = {};  // per device; guarded by g_mu
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return SOLATTN_ECUDA;
+  {
+    std::lock_guard<std::mutex> lk(g_mu);
+    if (!attr_set[dev]) {
+      if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem)) != cudaSuccess)
+        return SOLATTN_ECUDA;
+      attr_set[dev] = true;
+    }
+  }
+  const int half = 128 / a.G;
+  a.tile_tokens = 2 * half;
+  TileArgs x{};
+  // The uneven share of whole items is at most one item per block: below 1/6 of a block's work. A part
+  // costs about as much as two units of keys: a block's share of a split item is at least four.
+  x.min_units = 4, x.whole_items = kWholeItems;
+  CUtensorMap mq{}, mk{}, mv{};
+  if constexpr (!C::BITS8) {
+    const cuuint64_t ntok = a.cu ? a.total : a.n;
+    const cuuint64_t qd[5] = {D, static_cast<cuuint64_t>(a.G), ntok, static_cast<cuuint64_t>(a.Hkv),
+                              static_cast<cuuint64_t>(a.cu ? 1 : a.B)};
+    const long long qs[5] = {1, a.q_head, a.q_tok, a.q_head * a.G, a.q_batch};
+    const cuuint32_t qb[5] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(half), 1, 1};
+    const cuuint64_t kd[4] = {D, static_cast<cuuint64_t>(PAGED ? a.page : a.Lmax), static_cast<cuuint64_t>(a.Hkv),
+                              static_cast<cuuint64_t>(PAGED ? a.num_pages : a.B)};
+    const long long ks[4] = {1, a.k_row, a.k_head, a.k_seq}, vs[4] = {1, a.v_row, a.v_head, a.v_seq};
+    const cuuint32_t kb[4] = {64, static_cast<cuuint32_t>(PAGED ? a.page : kUnitKeys), 1, 1};
+    if (encode(&mq, dtype, 5, a.q, qd, qs, qb) != SOLATTN_OK || encode(&mk, dtype, 4, a.k, kd, ks, kb) != SOLATTN_OK ||
+        encode(&mv, dtype, 4, a.v, kd, vs, kb) != SOLATTN_OK)
+      return SOLATTN_ECUDA;
+    x.k_b = a.k_seq != 0, x.k_h = a.k_head != 0, x.v_b = a.v_seq != 0, x.v_h = a.v_head != 0;
+  }
+  cudaLaunchConfig_t cfg{};
+  cfg.gridDim = dim3(sms);
+  cfg.blockDim = dim3(C::THREADS);
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = st;
+  if (cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a, x) != cudaSuccess) return SOLATTN_ECUDA;
+  if (!launch(join_kernel<TokenTiles, QT, D, 64>, dim3(sms, TokenTiles::RT / 64), 256, st, true, a)) return SOLATTN_ECUDA;
+  return SOLATTN_OK;
+}
+
+template <class QT, int KIND, int D, bool PAGED>
+int dispatch_rows(const DenseArgs &a, int dtype, int rows, int sms, cudaStream_t st) {
+  constexpr int kind = KIND == kKind16 ? SOLATTN_CACHE_16 : KIND == kKindInt8 ? SOLATTN_CACHE_INT8 : SOLATTN_CACHE_E4M3;
+  if (rows > 16 && tile_fits(a, kind)) return launch_tiles<QT, KIND, D, PAGED>(a, dtype, sms, st);
   return rows <= 8 ? launch_rows<QT, KIND, D, 1, PAGED>(a, sms, st) : launch_rows<QT, KIND, D, 2, PAGED>(a, sms, st);
 }
 
 template <class QT, int D>
-int dispatch_kind(const DenseArgs &a, int kind, int rows, int sms, cudaStream_t st) {
-  if (!a.table) return dispatch_rows<QT, kKind16, D, false>(a, rows, sms, st);
-  if (kind == SOLATTN_CACHE_16) return dispatch_rows<QT, kKind16, D, true>(a, rows, sms, st);
-  if (kind == SOLATTN_CACHE_INT8) return dispatch_rows<QT, kKindInt8, D, true>(a, rows, sms, st);
-  return dispatch_rows<QT, kKindE4m3, D, true>(a, rows, sms, st);
+int dispatch_kind(const DenseArgs &a, int dtype, int kind, int rows, int sms, cudaStream_t st) {
+  if (!a.table) return dispatch_rows<QT, kKind16, D, false>(a, dtype, rows, sms, st);
+  if (kind == SOLATTN_CACHE_16) return dispatch_rows<QT, kKind16, D, true>(a, dtype, rows, sms, st);
+  if (kind == SOLATTN_CACHE_INT8) return dispatch_rows<QT, kKindInt8, D, true>(a, dtype, rows, sms, st);
+  return dispatch_rows<QT, kKindE4m3, D, true>(a, dtype, rows, sms, st);
 }
 
 int dispatch_dense(const DenseArgs &a, int d, int dtype, int kind, int rows, int sms, cudaStream_t st) {
   if (dtype == SOLATTN_BF16)
-    return d == 128 ? dispatch_kind<__nv_bfloat16, 128>(a, kind, rows, sms, st) : dispatch_kind<__nv_bfloat16, 64>(a, kind, rows, sms, st);
-  return d == 128 ? dispatch_kind<__half, 128>(a, kind, rows, sms, st) : dispatch_kind<__half, 64>(a, kind, rows, sms, st);
+    return d == 128 ? dispatch_kind<__nv_bfloat16, 128>(a, dtype, kind, rows, sms, st) : dispatch_kind<__nv_bfloat16, 64>(a, dtype, kind, rows, sms, st);
+  return d == 128 ? dispatch_kind<__half, 128>(a, dtype, kind, rows, sms, st) : dispatch_kind<__half, 64>(a, dtype, kind, rows, sms, st);
 }
 
 void set_workspace(DenseArgs *a, void *workspace, int d) {

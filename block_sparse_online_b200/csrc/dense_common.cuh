@@ -292,6 +292,8 @@ __device__ __forceinline__ uint32_t pack16<__nv_bfloat16>(float lo, float hi) { 
 template <>
 __device__ __forceinline__ uint32_t pack16<__half>(float lo, float hi) { return pack_f16x2(lo, hi); }
 
+__device__ __forceinline__ float u2f_(uint32_t x) { return __uint_as_float(x); }
+
 __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 

@@ -295,6 +295,13 @@ __device__ __forceinline__ float fmax3(float a, float b, float c) {
   return d;
 }
 
+// The same, but a NaN wins.
+__device__ __forceinline__ float fmax3_nan(float a, float b, float c) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Maximum of W values as a tree of three-input max instructions: depth log3(W) instead
 // of a dependent chain of W/2 (indices are compile-time after unrolling).
 template <int W>
@@ -358,6 +365,29 @@ __device__ __forceinline__ void exp2_poly_x2(float x0, float x1, float &y0, floa
   // Clamped to [-125, 64]: the exponent add below stays inside fp32's exponent range, so a
   // large input gives a large finite value (2^64) rather than a wrapped exponent.
   const uint64_t x = f2(fminf(fmaxf(x0, -125.f), 64.f), fminf(fmaxf(x1, -125.f), 64.f));
+  const uint64_t t = add2(x, f2(kShift, kShift));
+  const uint64_t nf = add2(t, f2(-kShift, -kShift));
+  const uint64_t fr = fma2(nf, f2(-1.f, -1.f), x);
+  uint64_t pp = fma2(fr, f2(c3, c3), f2(c2, c2));
+  pp = fma2(pp, fr, f2(c1, c1));
+  pp = fma2(pp, fr, f2(c0, c0));
+  float p0, p1, t0, t1;
+  f2_split(pp, p0, p1);
+  f2_split(t, t0, t1);
+  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
+  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
+}
+
+// The same, except that a NaN gives the largest finite number (fmin and fmax would drop it): the
+// clamps hand it through, and the integer sum below turns its bits into 0x7f7fffff.
+__device__ __forceinline__ void exp2_poly_nan_x2(float x0, float x1, float &y0, float &y1) {
+  constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
+  constexpr float c0 = 0.9999280571937561f, c1 = 0.6932609677314758f;
+  constexpr float c2 = 0.2426111251115799f, c3 = 0.0551716685295105f;
+  float a0, a1;
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(a0) : "f"(x0), "f"(-125.f), "f"(64.f));
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(a1) : "f"(x1), "f"(-125.f), "f"(64.f));
+  const uint64_t x = f2(a0, a1);
   const uint64_t t = add2(x, f2(kShift, kShift));
   const uint64_t nf = add2(t, f2(-kShift, -kShift));
   const uint64_t fr = fma2(nf, f2(-1.f, -1.f), x);

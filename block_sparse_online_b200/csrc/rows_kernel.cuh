@@ -113,11 +113,11 @@ struct RowsCfg {
 template <int ROWS, int D>
 struct RowsSmem {
   float m[kRowsWarps][ROWS], l[kRowsWarps][ROWS];
-  float o[kRowsWarps][ROWS][D + 4];
+  alignas(16) float o[kRowsWarps][ROWS][D + 4];
 };
 
 template <class QT, int KIND, int D, int NT, bool PAGED>
-__global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) rows_kernel(const DenseArgs a, int min_units, int whole_items) {
+__global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) rows_kernel(const __grid_constant__ DenseArgs a, int min_units, int whole_items) {
   using C = RowsCfg<QT, KIND, D, NT, PAGED>;
   using T = RowTiles<C::ROWS>;
   using MT = typename std::conditional<KIND == kKind16, QT, __half>::type;  // operands' type
