@@ -57,6 +57,7 @@ bool view_ok(const solattn_view *x, int elem, bool output, int64_t nb, int64_t n
 int check_device(std::initializer_list<const void *> ptrs, DeviceInfo *di) {
   if (device_info(di) != SOLATTN_OK) return SOLATTN_ECUDA;
   if (di->major != 10) return SOLATTN_EUNSUPPORTED;
+  if (di->devices == 1) return SOLATTN_OK;  // no other GPU for a pointer to belong to
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return SOLATTN_ECUDA;
   for (const void *p : ptrs)
@@ -108,13 +109,27 @@ bool launch(K kernel, dim3 grid, dim3 block, cudaStream_t st, bool dependent, Ar
 // items costs less than the parts' traffic.
 constexpr int kWholeItems = 6;
 
+// Whether some item may be split over blocks. It is not where no item has more units than the least
+// share of a block, nor where a uniform call has items enough; then nothing needs joining.
+template <class T>
+bool may_split(const DenseArgs &a, int blocks, int min_units) {
+  if (a.Lmax <= min_units * kUnitKeys) return false;
+  if (a.cu) return true;  // the host does not know the lengths
+  const long long per_head = T::RT == TokenTiles::RT ? (a.n + a.tile_tokens - 1) / a.tile_tokens
+                                                     : (static_cast<long long>(a.n) * a.G + T::RT - 1) / T::RT;
+  return per_head * a.B * a.Hkv < static_cast<long long>(kWholeItems) * blocks;
+}
+
 template <class QT, int KIND, int D, int NT, bool PAGED>
 int launch_rows(const DenseArgs &a, int sms, cudaStream_t st) {
   using T = RowTiles<8 * NT>;
   const int blocks = (NT == 1 ? 3 : 2) * sms;
   // A block's share is at least two units (256 keys) when the items alone do not fill the launch.
-  if (!launch(rows_kernel<QT, KIND, D, NT, PAGED>, blocks, kRowsWarps * 32, st, false, a, 2, kWholeItems)) return SOLATTN_ECUDA;
-  if (!launch(join_kernel<T, QT, D, T::RT>, blocks, 256, st, true, a)) return SOLATTN_ECUDA;
+  constexpr int min_units = 2;
+  const bool split = may_split<T>(a, blocks, min_units);
+  if (!launch(rows_kernel<QT, KIND, D, NT, PAGED>, blocks, kRowsWarps * 32, st, false, a, min_units, split ? kWholeItems : 0))
+    return SOLATTN_ECUDA;
+  if (split && !launch(join_kernel<T, QT, D, T::RT>, blocks, 256, st, true, a)) return SOLATTN_ECUDA;
   return SOLATTN_OK;
 }
 
@@ -175,7 +190,9 @@ int launch_tiles(DenseArgs a, int dtype, int sms, cudaStream_t st) {
   TileArgs x{};
   // The uneven share of whole items is at most one item per block: below 1/6 of a block's work. A part
   // costs about as much as two units of keys: a block's share of a split item is at least four.
-  x.min_units = 4, x.whole_items = kWholeItems;
+  x.min_units = 4;
+  const bool split = may_split<TokenTiles>(a, sms, x.min_units);
+  x.whole_items = split ? kWholeItems : 0;
   CUtensorMap mq{}, mk{}, mv{};
   if constexpr (!C::BITS8) {
     const cuuint64_t ntok = a.cu ? a.total : a.n;
@@ -198,7 +215,7 @@ int launch_tiles(DenseArgs a, int dtype, int sms, cudaStream_t st) {
   cfg.dynamicSmemBytes = smem;
   cfg.stream = st;
   if (cudaLaunchKernelEx(&cfg, kern, mq, mk, mv, a, x) != cudaSuccess) return SOLATTN_ECUDA;
-  if (!launch(join_kernel<TokenTiles, QT, D, 64>, dim3(sms, TokenTiles::RT / 64), 256, st, true, a)) return SOLATTN_ECUDA;
+  if (split && !launch(join_kernel<TokenTiles, QT, D, 32>, dim3(sms, TokenTiles::RT / 32), 256, st, true, a)) return SOLATTN_ECUDA;
   return SOLATTN_OK;
 }
 

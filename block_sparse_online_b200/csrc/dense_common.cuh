@@ -310,6 +310,41 @@ __global__ void __launch_bounds__(256) join_kernel(const DenseArgs a) {
   const int parts = rec.x;
   if (parts == 0) return;
   const Seq s = seq_of(a, rec.y);
+  if constexpr (T::RT == TokenTiles::RT) {
+    // Parts lie column group by column group: a warp reads 32 rows of a group of 4 columns
+    // at a time and the results turn through shared memory, so that rows are written whole.
+    __shared__ alignas(16) uint2 out[ROWS][D / 4 + 1];
+    static_assert(ROWS % 32 == 0 && 128 % ROWS == 0, "rows of a warp share a half");
+    for (int i = threadIdx.x; i < ROWS * (D / 4); i += 256) {
+      const int rl = i % ROWS, e = i / ROWS, r = blockIdx.y * ROWS + rl;
+      float m = -CUDART_INF_F;
+      for (int p = 0; p < parts; ++p) m = fmaxf(m, a.part_ml[static_cast<size_t>(p == 0 ? 2 * c + 1 : 2 * (c + p)) * 512 + r]);
+      float l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
+      const float ms = m == -CUDART_INF_F ? 0.f : m;
+      for (int p = 0; p < parts; ++p) {
+        const size_t sl = p == 0 ? 2 * c + 1 : 2 * (c + p);
+        const float w = ex2_approx(a.part_ml[sl * 512 + r] - ms);
+        l = fmaf(w, a.part_ml[sl * 512 + 256 + r], l);
+        const float4 x = *reinterpret_cast<const float4 *>(a.part_o + ((sl * 2 + (r >> 7)) * (D / 4) + e) * 512 + (r & 127) * 4);
+        o0 = fmaf(w, x.x, o0);
+        o1 = fmaf(w, x.y, o1);
+        o2 = fmaf(w, x.z, o2);
+        o3 = fmaf(w, x.w, o3);
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees no key is zero
+      out[rl][e] = make_uint2(pack16<QT>(o0 * inv, o1 * inv), pack16<QT>(o2 * inv, o3 * inv));
+    }
+    __syncthreads();
+    for (int i = threadIdx.x; i < ROWS * (D / 4); i += 256) {
+      const int rl = i / (D / 4), e = i % (D / 4);
+      int tok, g;
+      if (!T::row(a, s.n, rec.w, blockIdx.y * ROWS + rl, tok, g)) continue;
+      QT *dst = static_cast<QT *>(a.out) + rec.y * a.o_batch + static_cast<long long>(s.tok0 + tok) * a.o_tok +
+                static_cast<long long>(rec.z * a.G + g) * a.o_head + 4 * e;
+      *reinterpret_cast<uint2 *>(dst) = out[rl][e];
+    }
+    return;
+  }
   constexpr int TPR = D / 4;  // threads of a row
   const int e = threadIdx.x % TPR;
   for (int i = threadIdx.x / TPR; i < ROWS; i += 256 / TPR) {

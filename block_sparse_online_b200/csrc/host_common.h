@@ -32,6 +32,7 @@ struct NvtxRange {
 struct DeviceInfo {
   int sms = 0;
   int major = 0;
+  int devices = 0;  // GPUs of the process
   bool known = false;
 };
 
@@ -46,6 +47,9 @@ inline int device_info(DeviceInfo *out) {
     int sms = 0, major = 0;
     if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return SOLATTN_ECUDA;
     if (cudaDeviceGetAttribute(&major, cudaDevAttrComputeCapabilityMajor, dev) != cudaSuccess) return SOLATTN_ECUDA;
+    int devices = 0;
+    if (cudaGetDeviceCount(&devices) != cudaSuccess) return SOLATTN_ECUDA;
+    g_dev[dev].devices = devices;
     g_dev[dev].sms = sms;
     g_dev[dev].major = major;
     g_dev[dev].known = true;

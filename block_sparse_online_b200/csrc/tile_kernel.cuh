@@ -537,7 +537,8 @@ __device__ void tile_mma(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint
 // ------------------------------------------------------------------ softmax and epilogue
 
 template <class C>
-__device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint8_t *ring, int w, int warp, int lane) {
+__device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint8_t *q_smem, uint8_t *ring, int w, int warp,
+                             int lane) {
   constexpr int D = C::D;
   using QT = typename C::QT;
   using MT = typename C::MT;
@@ -586,7 +587,8 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
         release(kv + 2 * i);
         if (i > 0) release(kv + 2 * i - 1);
       }
-      if (i == n - 1 && (C::BITS8 || leader)) mbar_arrive(&sc.q_empty[qe % C::NQ]);
+      // (a complete tile keeps its queries' buffer for its output)
+      if (i == n - 1 && sg->part >= 0 && lane == 0) mbar_arrive(&sc.q_empty[qe % C::NQ]);
       const int base = (sg->u0 + i) * kUnitKeys, klim = sg->klim;
       const int left = lim - base;  // keys of this unit that the row sees
       const bool plain = __all_sync(0xffffffffu, left >= kUnitKeys);
@@ -755,8 +757,9 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
     kv += 2 * n;
     const float vm = C::BITS8 ? vref : 1.f;
     if (sg->part >= 0) {
+      // Partial result, [slot][half][column / 4][row][4]: a warp's stores are contiguous.
       const size_t slot = sg->part;
-      float *dst = a.part_o + (slot * 256 + w * 128 + row) * D;
+      float *dst = a.part_o + (slot * 2 + w) * (128 * D) + row * 4;
 #pragma unroll 1
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
@@ -765,34 +768,55 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
         reg_fence32(o);
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
-          *reinterpret_cast<float4 *>(dst + c * 32 + e) =
+          *reinterpret_cast<float4 *>(dst + (c * 8 + e / 4) * (128 * 4)) =
               make_float4(u2f_(o[e]) * vm, u2f_(o[e + 1]) * vm, u2f_(o[e + 2]) * vm, u2f_(o[e + 3]) * vm);
       }
       a.part_ml[slot * 512 + w * 128 + row] = m_ref;
       a.part_ml[slot * 512 + 256 + w * 128 + row] = l;
     } else {
+      // Complete rows: through this half's query buffer (every product with it is done), so that
+      // a warp writes whole rows: its 32 rows one by one would touch 32 lines with every
+      // store (measured: 3300 cycles a half, and the stores held up the barriers behind them).
       const float inv = l == 0.f ? 0.f : vm / l;  // a row that sees no key is zero
-      int tok, hg;
-      const bool row_ok = half_row(a, *sg, w, row, tok, hg);
-      uint4 *dst = reinterpret_cast<uint4 *>(static_cast<QT *>(a.out) + sg->b * a.o_batch +
-                                             static_cast<long long>(sg->tok + tok) * a.o_tok +
-                                             static_cast<long long>(sg->h * a.G + hg) * a.o_head);
-#pragma unroll 1
+      uint8_t *buf = q_smem + (qe % C::NQ) * C::HALF_BYTES;
+#pragma unroll
       for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         tmem_ld32(o_addr + c * 32, o);
         tmem_wait_ld();
         reg_fence32(o);
-        if (row_ok) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            uint32_t pk[4];
+        for (int e = 0; e < 4; ++e) {
+          uint32_t pk[4];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) pk[k] = pack16<QT>(u2f_(o[8 * e + 2 * k]) * inv, u2f_(o[8 * e + 2 * k + 1]) * inv);
-            st_global_v4_hint(dst + c * 4 + e, pk[0], pk[1], pk[2], pk[3], pol_out);
-          }
+          for (int k = 0; k < 4; ++k) pk[k] = pack16<QT>(u2f_(o[8 * e + 2 * k]) * inv, u2f_(o[8 * e + 2 * k + 1]) * inv);
+          *reinterpret_cast<uint4 *>(buf + swz(row, c * 4 + e)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
       }
+      tc_fence_before_sync();
+      mbar_arrive(&sc.o_empty[w]);
+      int tok, hg;
+      const bool row_ok = half_row(a, *sg, w, row, tok, hg);
+      unsigned long long dst = reinterpret_cast<unsigned long long>(
+          static_cast<QT *>(a.out) + sg->b * a.o_batch + static_cast<long long>(sg->tok + tok) * a.o_tok +
+          static_cast<long long>(sg->h * a.G + hg) * a.o_head);
+      if (!row_ok) dst = 0;
+      __syncwarp();
+      constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows of a store
+      const int ch = lane % LPR;
+#pragma unroll 4
+      for (int r = 0; r < 32; r += RPI) {
+        const int rr = r + lane / LPR;
+        const unsigned long long p = __shfl_sync(0xffffffffu, dst, rr);
+        const uint4 v = *reinterpret_cast<const uint4 *>(buf + swz(wq * 32 + rr, ch));
+        if (p) st_global_v4_hint(reinterpret_cast<uint4 *>(p) + ch, v.x, v.y, v.z, v.w, pol_out);
+      }
+      // The next copy into the buffer is ordered behind these reads.
+      fence_proxy_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sc.q_empty[qe % C::NQ]);
+      rd.done(sc);
+      continue;
     }
     tc_fence_before_sync();
     mbar_arrive(&sc.o_empty[w]);
@@ -822,7 +846,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     for (int i = 0; i < C::NQ; ++i) {
       mbar_init(&sc.q_full[i], fillers);
-      mbar_init(&sc.q_empty[i], C::BITS8 ? 128 : 1);
+      mbar_init(&sc.q_empty[i], 4);  // the half's softmax warps
     }
     for (int w = 0; w < 2; ++w) {
       mbar_init(&sc.s_full[w], 1);
@@ -877,7 +901,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       tile_mma<C>(sc, a, tmem, q_smem, ring, warp == 1 ? 0 : 1);
     }
   } else if (warp < 12) {
-    tile_softmax<C>(sc, a, tmem, ring, (warp - 4) >> 2, warp, lane);
+    tile_softmax<C>(sc, a, tmem, q_smem, ring, (warp - 4) >> 2, warp, lane);
   } else if constexpr (C::BITS8) {
     tile_converter<C>(sc, a, q_smem, ring);
   }

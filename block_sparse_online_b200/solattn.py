@@ -495,38 +495,67 @@ def solattn_selftest_exp2(x: torch.Tensor, stream=None) -> torch.Tensor:
 # ---------------------------------------------------------------- dense attention and the cache
 
 
-def _rows(x, name, dtypes, shape, device):
-    """A strided tensor of rows of d contiguous elements; returns its type."""
+def _rows(x, name, dtype, shape, device):
+    """Checks a strided tensor of rows of d contiguous elements and returns its strides. The
+    usual case passes on one line: these calls take a few microseconds on the GPU."""
+    if isinstance(x, torch.Tensor) and x.dtype is dtype and x.shape == shape and x.device == device:
+        st = x.stride()
+        if st[-1] == 1 or not x.numel():
+            return st
+        raise ValueError(f"the last dimension of {name} must be contiguous")
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if x.dtype not in dtypes:
-        raise ValueError(f"{name} must have dtype {' or '.join(str(d) for d in dtypes)}, not {x.dtype}")
-    if not x.is_cuda or (device is not None and x.device != device):
-        raise ValueError(f"{name} is on {x.device}, " + (f"the inputs on {device}" if device else "not on a CUDA device"))
-    if tuple(x.shape) != tuple(shape):
+    if x.dtype is not dtype:
+        raise ValueError(f"{name} must have dtype {dtype}, not {x.dtype}")
+    if x.shape != shape:
         raise ValueError(f"{name} has shape {tuple(x.shape)}, {tuple(shape)} expected")
-    if x.numel() and x.stride(-1) != 1:
-        raise ValueError(f"the last dimension of {name} must be contiguous")
+    raise ValueError(f"{name} is on {x.device}, the inputs on {device}")
 
 
-def _view4(x):  # [B, heads, n, d]
-    st = x.stride()
-    return _View(x.data_ptr() or None, st[0], st[1], st[2])
+def _view4(x, name, dtype, shape, device):  # [B, heads, n, d]
+    st = _rows(x, name, dtype, shape, device)
+    return _View(x.data_ptr(), st[0], st[1], st[2])
 
 
-def _view3(x):  # packed rows [n, heads, d]
-    st = x.stride()
-    return _View(x.data_ptr() or None, 0, st[1], st[0])
+def _view3(x, name, dtype, shape, device):  # packed rows [n, heads, d]
+    st = _rows(x, name, dtype, shape, device)
+    return _View(x.data_ptr(), 0, st[1], st[0])
+
+
+def _int32(x, name, numel, device):
+    if not (isinstance(x, torch.Tensor) and x.dtype is torch.int32 and x.device == device and x.is_contiguous()
+            and x.numel() >= numel):
+        _check_buffer(x, name, (torch.int32,), numel, device)
+    return x.data_ptr()
 
 
 def _workspace(workspace, need, device):
-    """The caller's workspace, or a new one with its header cleared."""
+    """The caller's workspace (the library checks its size), or a new one with its header cleared."""
     if workspace is None:
-        workspace = torch.empty(need, dtype=torch.uint8, device=device)
+        workspace = torch.empty(need(), dtype=torch.uint8, device=device)
         workspace[:256].zero_()
-        return workspace
-    _check_buffer(workspace, "workspace", (torch.uint8, torch.int8), need, device)
+    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and workspace.device == device
+              and workspace.is_contiguous()):
+        _check_buffer(workspace, "workspace", (torch.uint8, torch.int8), 0, device)
     return workspace
+
+
+def _on_device(device, stream, call, *args):
+    """call(*args, stream) with `device` current; the stream is the caller's or the current one."""
+    if stream is not None:
+        handle = _stream(stream, device)
+    else:
+        handle = torch._C._cuda_getCurrentRawStream(device.index)
+    if torch.cuda.current_device() == device.index:
+        return call(*args, handle)
+    with torch.cuda.device(device):
+        return call(*args, handle)
+
+
+def _need(size, what):
+    if size == 0:
+        raise SolAttnError(SOLATTN_EUNSUPPORTED, what)
+    return size
 
 
 def alloc_status(device="cuda") -> torch.Tensor:
@@ -545,10 +574,8 @@ def solattn_paged_workspace_size(B, H, Hkv, total, d) -> int:
 
 def alloc_cross_workspace(B, H, Hkv, Nq, Nk, d, device="cuda") -> torch.Tensor:
     """Workspace of :func:`solattn_cross`, its status word cleared."""
-    n = solattn_cross_workspace_size(B, H, Hkv, Nq, Nk, d)
-    if n == 0:
-        raise SolAttnError(SOLATTN_EUNSUPPORTED, "solattn_cross_workspace_size")
-    return _workspace(None, n, device)
+    return _workspace(None, lambda: _need(solattn_cross_workspace_size(B, H, Hkv, Nq, Nk, d), "solattn_cross_workspace_size"),
+                      device)
 
 
 def solattn_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_len: torch.Tensor | None = None,
@@ -560,27 +587,22 @@ def solattn_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_len: to
     may hold anything); a sequence of none gives zeros. H is a multiple of Hkv: query head h
     uses key head h // (H // Hkv). Returns out [B, H, Nq, d]. Asynchronous on ``stream``;
     lengths outside [0, Nk] are reported by :func:`solattn_get_status` on the workspace."""
-    B, H, Nq, d = _bhnd(q)
-    Hkv, Nk = (int(k.shape[1]), int(k.shape[2])) if isinstance(k, torch.Tensor) and k.dim() == 4 else (0, 0)
-    if q.dtype not in DTYPES:
-        raise ValueError(f"q must be bfloat16 or float16, not {q.dtype}")
-    dev, one = q.device, (q.dtype,)
-    _rows(q, "q", one, (B, H, Nq, d), None)
-    _rows(k, "k", one, (B, Hkv, Nk, d), dev)
-    _rows(v, "v", one, (B, Hkv, Nk, d), dev)
+    dt = DTYPES.get(getattr(q, "dtype", None))
+    if dt is None or not q.is_cuda or q.dim() != 4:
+        raise ValueError("q must be a bfloat16 or float16 [B, H, N, d] CUDA tensor")
+    if not isinstance(k, torch.Tensor) or k.dim() != 4:
+        raise ValueError("k must be a [B, Hkv, Nk, d] tensor")
+    dtype, dev, shape = q.dtype, q.device, q.shape
+    B, H, Nq, d = shape
+    Hkv, Nk = k.shape[1], k.shape[2]
+    kshape = (B, Hkv, Nk, d)
     if out is None:
-        out = torch.empty_like(q) if 0 not in q.stride() else torch.empty((B, H, Nq, d), dtype=q.dtype, device=dev)
-    _rows(out, "out", one, (B, H, Nq, d), dev)
-    if key_len is not None:
-        _check_buffer(key_len, "key_len", (torch.int32,), B, dev)
-    need = solattn_cross_workspace_size(B, H, Hkv, Nq, Nk, d)
-    if need == 0:
-        raise SolAttnError(SOLATTN_EUNSUPPORTED, "solattn_cross")
-    workspace = _workspace(workspace, need, dev)
-    with torch.cuda.device(dev):
-        rc = _lib.solattn_cross(_view4(q), _view4(k), _view4(v), _view4(out),
-                                key_len.data_ptr() if key_len is not None else None, B, H, Hkv, Nq, Nk, d,
-                                DTYPES[q.dtype], workspace.data_ptr(), workspace.numel(), _stream(stream, dev))
+        out = torch.empty_like(q) if 0 not in q.stride() else torch.empty(shape, dtype=dtype, device=dev)
+    workspace = _workspace(workspace, lambda: _need(solattn_cross_workspace_size(B, H, Hkv, Nq, Nk, d), "solattn_cross"), dev)
+    rc = _on_device(dev, stream, _lib.solattn_cross, _view4(q, "q", dtype, shape, dev), _view4(k, "k", dtype, kshape, dev),
+                    _view4(v, "v", dtype, kshape, dev), _view4(out, "out", dtype, shape, dev),
+                    None if key_len is None else _int32(key_len, "key_len", B, dev), B, H, Hkv, Nq, Nk, d, dt,
+                    workspace.data_ptr(), workspace.numel())
     _check(rc, "solattn_cross")
     return out
 
@@ -594,46 +616,48 @@ class PagedCache:
 
     def __init__(self, k_pages: torch.Tensor, v_pages: torch.Tensor, k_scale: torch.Tensor | None = None,
                  v_scale: torch.Tensor | None = None):
-        P, Hkv, page, d = _bhnd(k_pages)
-        dt = k_pages.dtype
+        P, Hkv, page, d = shape = _bhnd(k_pages)
+        dt, dev = k_pages.dtype, k_pages.device
         if dt not in DTYPES and dt not in CACHE_KINDS:
             raise ValueError(f"pages must be bfloat16, float16, int8 or float8_e4m3fn, not {dt}")
-        _rows(k_pages, "k_pages", (dt,), (P, Hkv, page, d), None)
-        _rows(v_pages, "v_pages", (dt,), (P, Hkv, page, d), k_pages.device)
+        if not k_pages.is_cuda:
+            raise ValueError("the pages must be CUDA tensors")
+        k, v = _view4(k_pages, "k_pages", dt, shape, dev), _view4(v_pages, "v_pages", dt, shape, dev)
         if (dt in CACHE_KINDS) != (k_scale is not None) or (dt in CACHE_KINDS) != (v_scale is not None):
             raise ValueError("8-bit pages need k_scale and v_scale, 16-bit pages take none")
         for name, sc in (("k_scale", k_scale), ("v_scale", v_scale)):
             if sc is not None:
-                _check_buffer(sc, name, (torch.float32,), P * Hkv * page, k_pages.device)
+                _check_buffer(sc, name, (torch.float32,), P * Hkv * page, dev)
                 if tuple(sc.shape) != (P, Hkv, page):
                     raise ValueError(f"{name} has shape {tuple(sc.shape)}, {(P, Hkv, page)} expected")
         self.k_pages, self.v_pages, self.k_scale, self.v_scale = k_pages, v_pages, k_scale, v_scale
-        self.num_pages, self.Hkv, self.page, self.d, self.dtype, self.device = P, Hkv, page, d, dt, k_pages.device
-        self._c = _Cache(_view4(k_pages), _view4(v_pages), None if k_scale is None else k_scale.data_ptr(),
+        self.num_pages, self.Hkv, self.page, self.d, self.dtype, self.device = P, Hkv, page, d, dt, dev
+        self._c = _Cache(k, v, None if k_scale is None else k_scale.data_ptr(),
                          None if v_scale is None else v_scale.data_ptr(), P, Hkv, page, d, CACHE_KINDS.get(dt, 0))
 
     def _seqs(self, table, cu, length, total):
         """The sequences of a call, checked."""
         if not isinstance(table, torch.Tensor) or table.dim() != 2:
             raise ValueError("table must be an int32 [B, width] tensor")
-        B, width = int(table.shape[0]), int(table.shape[1])
-        _check_buffer(table, "table", (torch.int32,), max(1, B * width), self.device)
-        _check_buffer(cu, "cu", (torch.int32,), B + 1, self.device)
-        _check_buffer(length, "length", (torch.int32,), B, self.device)
-        return _Seqs(table.data_ptr(), cu.data_ptr(), length.data_ptr(), B, width, total)
+        B, width = table.shape
+        dev = self.device
+        return _Seqs(_int32(table, "table", 1, dev), _int32(cu, "cu", B + 1, dev), _int32(length, "length", B, dev), B,
+                     width, total)
 
-    def _check_rows(self, x, name, total, dtype):
-        if dtype not in DTYPES or (self.dtype in DTYPES and dtype != self.dtype):
+    def _rows_dtype(self, x, name):
+        """The 16-bit type of packed rows x [total, heads, d], and how many they are."""
+        if not isinstance(x, torch.Tensor) or x.dim() != 3:
+            raise ValueError(f"{name} must be a [total, heads, d] tensor")
+        dtype = x.dtype
+        if dtype not in DTYPES or (self.dtype in DTYPES and dtype is not self.dtype):
             raise ValueError(f"{name} must be " + (str(self.dtype) if self.dtype in DTYPES else "bfloat16 or float16"))
-        _rows(x, name, (dtype,), (total, self.Hkv, self.d), self.device)
+        return dtype, x.shape[0]
 
 
 def alloc_paged_workspace(cache: PagedCache, B, H, total, device=None) -> torch.Tensor:
     """Workspace of :func:`solattn_paged_forward`, its status word cleared."""
-    n = solattn_paged_workspace_size(B, H, cache.Hkv, total, cache.d)
-    if n == 0:
-        raise SolAttnError(SOLATTN_EUNSUPPORTED, "solattn_paged_workspace_size")
-    return _workspace(None, n, cache.device if device is None else device)
+    return _workspace(None, lambda: _need(solattn_paged_workspace_size(B, H, cache.Hkv, total, cache.d),
+                                          "solattn_paged_workspace_size"), cache.device if device is None else device)
 
 
 def solattn_paged_forward(q: torch.Tensor, cache: PagedCache, table: torch.Tensor, cu: torch.Tensor,
@@ -647,24 +671,19 @@ def solattn_paged_forward(q: torch.Tensor, cache: PagedCache, table: torch.Tenso
     ``max_new``: the most new tokens of a sequence, as far as the caller knows (it selects the
     kernel, not the result). Rows behind cu[B] are left alone. Returns out [total, H, d].
     Lengths or pages out of range are reported by :func:`solattn_get_status` on the workspace."""
-    if not isinstance(q, torch.Tensor) or q.dim() != 3:
-        raise ValueError("q must be a [total, H, d] tensor")
-    total, H = int(q.shape[0]), int(q.shape[1])
-    if q.dtype not in DTYPES or (cache.dtype in DTYPES and q.dtype != cache.dtype):
-        raise ValueError("q must be " + (str(cache.dtype) if cache.dtype in DTYPES else "bfloat16 or float16"))
-    dev = cache.device
-    _rows(q, "q", (q.dtype,), (total, H, cache.d), dev)
+    if not isinstance(cache, PagedCache):
+        raise ValueError("cache must be a PagedCache")
+    dtype, total = cache._rows_dtype(q, "q")
+    dev, H = cache.device, q.shape[1]
+    shape = (total, H, cache.d)
     if out is None:
-        out = torch.empty((total, H, cache.d), dtype=q.dtype, device=dev)
-    _rows(out, "out", (q.dtype,), (total, H, cache.d), dev)
+        out = torch.empty(shape, dtype=dtype, device=dev)
     seqs = cache._seqs(table, cu, length, total)
-    need = solattn_paged_workspace_size(seqs.B, H, cache.Hkv, total, cache.d)
-    if need == 0:
-        raise SolAttnError(SOLATTN_EUNSUPPORTED, "solattn_paged_forward")
-    workspace = _workspace(workspace, need, dev)
-    with torch.cuda.device(dev):
-        rc = _lib.solattn_paged_forward(_view3(q), _view3(out), cache._c, seqs, H, int(max_new), int(bool(causal)),
-                                        DTYPES[q.dtype], workspace.data_ptr(), workspace.numel(), _stream(stream, dev))
+    workspace = _workspace(workspace, lambda: _need(solattn_paged_workspace_size(seqs.B, H, cache.Hkv, total, cache.d),
+                                                    "solattn_paged_forward"), dev)
+    rc = _on_device(dev, stream, _lib.solattn_paged_forward, _view3(q, "q", dtype, shape, dev),
+                    _view3(out, "out", dtype, shape, dev), cache._c, seqs, H, int(max_new), 1 if causal else 0, DTYPES[dtype],
+                    workspace.data_ptr(), workspace.numel())
     _check(rc, "solattn_paged_forward")
     return out
 
@@ -675,14 +694,12 @@ def solattn_cache_append(cache: PagedCache, new_k: torch.Tensor, new_v: torch.Te
     quantised where the cache is 8-bit: scale = max|x| / TOP, code = nearest(x TOP / max|x|), TOP = 127
     (int8) or 448 (e4m3). table, cu, length as in :func:`solattn_paged_forward` (length counts
     the new tokens). ``workspace``: an :func:`alloc_status` tensor or any workspace."""
-    total = int(new_k.shape[0]) if isinstance(new_k, torch.Tensor) and new_k.dim() == 3 else -1
-    cache._check_rows(new_k, "new_k", total, getattr(new_k, "dtype", None))
-    cache._check_rows(new_v, "new_v", total, new_k.dtype)
+    dtype, total = cache._rows_dtype(new_k, "new_k")
+    dev, shape = cache.device, (total, cache.Hkv, cache.d)
     seqs = cache._seqs(table, cu, length, total)
-    workspace = _workspace(workspace, 256, cache.device)
-    with torch.cuda.device(cache.device):
-        rc = _lib.solattn_cache_append(cache._c, _view3(new_k), _view3(new_v), seqs, DTYPES[new_k.dtype],
-                                       workspace.data_ptr(), _stream(stream, cache.device))
+    workspace = _workspace(workspace, lambda: 256, dev)
+    rc = _on_device(dev, stream, _lib.solattn_cache_append, cache._c, _view3(new_k, "new_k", dtype, shape, dev),
+                    _view3(new_v, "new_v", dtype, shape, dev), seqs, DTYPES[dtype], workspace.data_ptr())
     _check(rc, "solattn_cache_append")
 
 
@@ -690,14 +707,12 @@ def solattn_cache_read(cache: PagedCache, table: torch.Tensor, cu: torch.Tensor,
                        k_out: torch.Tensor, v_out: torch.Tensor, workspace: torch.Tensor | None = None, stream=None):
     """Reads the new tokens' rows (the last cu[b+1] - cu[b] of each sequence) back from the pages into
     k_out and v_out [total, Hkv, d] (bf16 or fp16): code * scale, rounded once. Returns them."""
-    total = int(k_out.shape[0]) if isinstance(k_out, torch.Tensor) and k_out.dim() == 3 else -1
-    cache._check_rows(k_out, "k_out", total, getattr(k_out, "dtype", None))
-    cache._check_rows(v_out, "v_out", total, k_out.dtype)
+    dtype, total = cache._rows_dtype(k_out, "k_out")
+    dev, shape = cache.device, (total, cache.Hkv, cache.d)
     seqs = cache._seqs(table, cu, length, total)
-    workspace = _workspace(workspace, 256, cache.device)
-    with torch.cuda.device(cache.device):
-        rc = _lib.solattn_cache_read(cache._c, seqs, _view3(k_out), _view3(v_out), DTYPES[k_out.dtype],
-                                     workspace.data_ptr(), _stream(stream, cache.device))
+    workspace = _workspace(workspace, lambda: 256, dev)
+    rc = _on_device(dev, stream, _lib.solattn_cache_read, cache._c, seqs, _view3(k_out, "k_out", dtype, shape, dev),
+                    _view3(v_out, "v_out", dtype, shape, dev), DTYPES[dtype], workspace.data_ptr())
     _check(rc, "solattn_cache_read")
     return k_out, v_out
 
