@@ -16,7 +16,10 @@
 //                unit they zero the value rows behind the end, which may hold anything (0 times NaN is NaN).
 //   warps 12-15  8-bit keys only: read codes from the pages, expand them to fp16 into the ring (and the
 //                queries, scaled, into their buffers), one unit ahead in registers.
-// S and P of a half share their columns: S(u+1) is computed after P V(u) has read P(u).
+// A step is 64 keys. Each half has two buffers of S (P takes the place of its S): Q K^T of step j + 2
+// follows P V of step j, so while a warpgroup exponentiates step j + 1 the tensor core works on its steps
+// j and j + 2. With one buffer of 128 keys instead, S, softmax and P V formed one chain of 3700 cycles a
+// unit (the tensor core needs 2048 for both halves).
 //
 // Softmax: once a row has a reference maximum a unit is exponentiated against it without taking the row
 // maximum; a row sum <= 2^15 shows that no value is large, otherwise (or for a row's first
@@ -52,24 +55,27 @@ struct TileCfg {
   static constexpr int NQ = BITS8 ? 2 : 3;
   static constexpr int NSLOT = D == 128 ? 4 : 8;
   static constexpr int NSC = 4;  // units whose scales are kept
-  static constexpr int COLS = 128 + D;  // tensor memory columns of a half: S (and P), O
-  static constexpr int TMEM_COLS = 2 * COLS <= 256 ? 256 : 512;
+  static constexpr int COLS = 128 + D;  // tensor memory columns of a half: O, two buffers of S (and P)
+  static constexpr int TMEM_COLS = 512;
   static constexpr int THREADS = BITS8 ? 512 : 384;
   // Register shares: within what the block is launched with (384 x 168, 512 x 128).
-  static constexpr int CTRL_REGS = BITS8 ? 80 : 104;
-  static constexpr int CONV_REGS = 112;
-  static constexpr int SOFTMAX_REGS = BITS8 ? 160 : 200;
+  static constexpr int CTRL_REGS = BITS8 ? 72 : 104;
+  static constexpr int CONV_REGS = 136;
+  static constexpr int SOFTMAX_REGS = BITS8 ? 152 : 200;
+  static_assert(CTRL_REGS < (BITS8 ? 128 : 168) && CONV_REGS > 128 && SOFTMAX_REGS > (BITS8 ? 128 : 168),
+                "control warps give registers up, the others take them");
   static_assert(BITS8 ? 128 * CTRL_REGS + 128 * CONV_REGS + 256 * SOFTMAX_REGS <= 512 * 128
                       : 128 * CTRL_REGS + 256 * SOFTMAX_REGS <= 384 * 168, "register split");
   static constexpr bool FP16 = std::is_same<MT, __half>::value;
   static constexpr uint32_t IDESC_PV = idesc_16bit_f32(128, D, true, FP16);
 };
 
+constexpr int kStepKeys = 64;  // keys of a step: a unit is two (the last may be one)
 constexpr int kSegs = 4;  // segments published ahead
 
 // A segment of the block's range: units u0 .. u1 - 1 of one tile.
 struct Segment {
-  int n, u0, klim, L;   // units (0: no more work), first unit, keys that some row sees, keys
+  int n, ns, u0, klim, L;  // units (0: no more work), steps, first unit, keys that some row sees, keys
   int tok, end;         // the tile's first query row in Q and out, and its sequence's end there
   int b, h, lim0;       // lim0: keys that the tile's first token sees
   int part;             // workspace slot of a partial result, or -1
@@ -81,7 +87,7 @@ struct TileCtl {
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t full[C::NSLOT], empty[C::NSLOT];
   uint64_t q_full[C::NQ], q_empty[C::NQ];
-  uint64_t s_full[2], p_full[2], o_full[2], o_empty[2];
+  uint64_t s_full[2][2], p_full[2][2], o_empty[2];  // by half, and buffer of S
   uint64_t conv;  // the converter's four warps
   uint64_t mma_done[2];
   uint32_t turn;
@@ -91,7 +97,7 @@ struct TileCtl {
   alignas(16) float ks[C::BITS8 ? C::NSC : 1][C::BITS8 ? 128 : 4];  // key scales (x log2(e) / sqrt d)
   alignas(16) float vs[C::BITS8 ? C::NSC : 1][C::BITS8 ? 128 : 4];  // value scales over the reference
   float vgrow[C::NSC], vref[C::NSC];  // factor of O when the reference grew, and the reference
-  alignas(16) float qdown[C::BITS8 ? C::NQ : 1][C::BITS8 ? 128 : 4];  // what a query row was divided by
+  uint32_t qmax[4];              // converter: largest query of the tile per warp (bf16 bits)
 };
 
 template <class C>
@@ -128,12 +134,9 @@ struct TileArgs {
   int min_units, whole_items;
 };
 
-// Steps of 16 keys that a unit's products need: some row of the tile sees a key in each.
-__device__ __forceinline__ int unit_steps(int klim, int u) { return min(8, max(1, (klim - u * kUnitKeys + 15) >> 4)); }
-// Whether value rows of the unit's last step lie behind the sequence's end.
-__device__ __forceinline__ bool unit_ragged(int L, int klim, int u) {
-  return L < u * kUnitKeys + 16 * unit_steps(klim, u);
-}
+// Slices of 16 keys that the products of the step at key `base` need: some row of the tile sees
+// a key in each.
+__device__ __forceinline__ int step_slices(int klim, int base) { return min(4, max(1, (klim - base + 15) >> 4)); }
 
 // ------------------------------------------------------------------ segments
 
@@ -155,6 +158,7 @@ __device__ void tile_scheduler(TileCtl<C> &sc, const DenseArgs &a, const TileArg
       g.n = cur.u1 - cur.u0;
       g.u0 = cur.u0;
       g.klim = key_limit(a, s, TokenTiles::last_token(a, s.n, cur.t));
+      g.ns = 2 * g.n - (g.klim - (cur.u1 - 1) * kUnitKeys <= kStepKeys ? 1 : 0);
       g.L = s.L;
       g.tok = s.tok0 + cur.t * a.tile_tokens;
       g.end = s.tok0 + s.n;
@@ -290,7 +294,7 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
   const volatile int *ab = &sc.abort_flag;
   const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
   const int rl = tid / LPR, pc = tid % LPR;
-  uint32_t kv = 0, qi = 0, tile = 0;
+  uint32_t kv = 0, qi = 0, tile = 0, conv_ph = 0;
   bool ok = true;
   auto wait = [&](uint64_t *bar, uint32_t par) {
     bool w = mbar_wait(bar, par, a.timeout_ns, ab);
@@ -298,10 +302,10 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
     if (!w) ok = false;
     return w;
   };
-  uint4 cd[NP];
+  uint4 ck[NP], cv[NP];  // codes of the next unit's keys and values
   float ksc, vsc;
   // Codes of a unit's keys or values into registers.
-  auto fetch = [&](const Segment &c, int u, bool is_v) {
+  auto fetch = [&](const Segment &c, int u, bool is_v, uint4(&cd)[NP]) {
     const uint8_t *base = static_cast<const uint8_t *>(is_v ? a.v : a.k) + c.h * (is_v ? a.v_head : a.k_head) + pc * 16;
     const long long row = is_v ? a.v_row : a.k_row, seq = is_v ? a.v_seq : a.k_seq;
 #pragma unroll
@@ -321,7 +325,7 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
     ksc = id >= 0 ? __ldg(a.k_scale + at) : 0.f;
     vsc = id >= 0 ? __ldg(a.v_scale + at) : 0.f;
   };
-  auto expand = [&](uint8_t *dst) {
+  auto expand = [&](uint8_t *dst, const uint4(&cd)[NP]) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int r = i * RPP + rl;
@@ -348,37 +352,60 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
   SegmentReader<C> rd;
   const Segment *g = rd.next_warp(sc, a, ok);
   if (g) {
-    fetch(*g, g->u0, false);
+    fetch(*g, g->u0, false, ck);
     fetch_scales(*g, g->u0);
+    fetch(*g, g->u0, true, cv);
   }
   while (g) {
-    // ---- queries of both halves, a row per thread, scaled to fp16
+    // ---- queries of both halves, a row of each per thread. bf16 queries become fp16 after a division of the
+    // tile by one power of two, which brings its largest finite element to [2^14, 2^15): elements down to
+    // 2^-31 of that are exact, and a smaller one is off by 2^-39 of it, which no logit shows. The factor
+    // goes into the key scales.
+    float up = 1.f, down = 1.f;
+    const typename C::QT *src[2];
+    bool row_ok[2];
+#pragma unroll
+    for (int w = 0; w < 2; ++w) {
+      int tok, hg;
+      row_ok[w] = half_row(a, *g, w, tid, tok, hg);
+      src[w] = static_cast<const typename C::QT *>(a.q) + static_cast<long long>(g->tok + tok) * a.q_tok +
+               static_cast<long long>(g->h * a.G + hg) * a.q_head;
+    }
+    if constexpr (std::is_same<typename C::QT, __nv_bfloat16>::value) {
+      uint32_t big = 0;
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+#pragma unroll 2
+        for (int i = 0; i < D / 8; ++i) {
+          const uint4 v = row_ok[w] ? __ldg(reinterpret_cast<const uint4 *>(src[w]) + i) : make_uint4(0, 0, 0, 0);
+          const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            const uint32_t lo = vv[e] & 0x7fffu, hi = (vv[e] >> 16) & 0x7fffu;
+            big = max(big, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+          }
+        }
+      }
+      big = __reduce_max_sync(0xffffffffu, big);
+      if (lane == 0) {
+        sc.qmax[warp] = big;
+        mbar_arrive(&sc.conv);
+      }
+      if (!wait(&sc.conv, conv_ph)) break;
+      conv_ph ^= 1;
+      big = max(max(sc.qmax[0], sc.qmax[1]), max(sc.qmax[2], sc.qmax[3]));
+      const int ex = static_cast<int>(big >> 7);  // biased exponent
+      const int sh = ex == 0 ? 0 : min(max(141 - ex, -126), 126);
+      up = __int_as_float((127 + sh) << 23);
+      down = __int_as_float((127 - sh) << 23);
+    }
     for (int w = 0; w < 2 && ok; ++w) {
       const int sl = qi % C::NQ;
       if (!wait(&sc.q_empty[sl], ((qi / C::NQ) & 1) ^ 1)) break;
-      int tok, hg;
-      const bool row_ok = half_row(a, *g, w, tid, tok, hg);
-      const typename C::QT *src = static_cast<const typename C::QT *>(a.q) + static_cast<long long>(g->tok + tok) * a.q_tok +
-                                  static_cast<long long>(g->h * a.G + hg) * a.q_head;
       uint8_t *dst = q_smem + sl * C::HALF_BYTES;
-      float down = 1.f, up = 1.f;
-      if constexpr (std::is_same<typename C::QT, __nv_bfloat16>::value) {
-        uint32_t big = 0;
-#pragma unroll 4
-        for (int i = 0; i < D / 8; ++i) {
-          const uint4 v = row_ok ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0, 0, 0, 0);
-          const uint32_t vv[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-          for (int e = 0; e < 4; ++e) big = max(big, max(vv[e] & 0x7fffu, (vv[e] >> 16) & 0x7fffu));
-        }
-        const int ex = static_cast<int>(big >> 7);
-        const int sh = (ex == 0 || ex == 255) ? 0 : min(max(141 - ex, -126), 126);
-        up = __int_as_float((127 + sh) << 23);
-        down = __int_as_float((127 - sh) << 23);
-      }
-#pragma unroll 4
+#pragma unroll 2
       for (int i = 0; i < D / 8; ++i) {
-        uint4 v = row_ok ? __ldg(reinterpret_cast<const uint4 *>(src) + i) : make_uint4(0, 0, 0, 0);
+        uint4 v = row_ok[w] ? __ldg(reinterpret_cast<const uint4 *>(src[w]) + i) : make_uint4(0, 0, 0, 0);
         if constexpr (std::is_same<typename C::QT, __nv_bfloat16>::value) {
           v.x = pack_f16x2(__uint_as_float(v.x << 16) * up, __uint_as_float(v.x & 0xffff0000u) * up);
           v.y = pack_f16x2(__uint_as_float(v.y << 16) * up, __uint_as_float(v.y & 0xffff0000u) * up);
@@ -387,11 +414,11 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
         }
         *reinterpret_cast<uint4 *>(dst + swz(tid, i)) = v;
       }
-      sc.qdown[sl][tid] = down;
       publish(&sc.q_full[sl]);
       ++qi;
     }
     if (!ok) break;
+    const float kmul = a.scale_log2 * down;
     // ---- units: K u, then V u, each with the next piece's codes on their way
     float vref = 0.f;
     const Segment *nxt = nullptr;
@@ -407,7 +434,8 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
         sc.wmax[tile & 1][warp] = mx;
         mbar_arrive(&sc.conv);
       }
-      if (!wait(&sc.conv, tile & 1)) break;
+      if (!wait(&sc.conv, conv_ph)) break;
+      conv_ph ^= 1;
       mx = fmaxf(fmaxf(sc.wmax[tile & 1][0], sc.wmax[tile & 1][1]), fmaxf(sc.wmax[tile & 1][2], sc.wmax[tile & 1][3]));
       float growth = 1.f;
       if (mx > vref) {
@@ -417,30 +445,31 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
         vref = vnew;
       }
       const int ss = tile % C::NSC;
-      sc.ks[ss][tid] = ksc * a.scale_log2;
+      sc.ks[ss][tid] = ksc * kmul;
       sc.vs[ss][tid] = vref > 0.f ? vsc * __int_as_float((254 << 23) - __float_as_int(vref)) : vsc;
       if (tid == 0) sc.vgrow[ss] = growth, sc.vref[ss] = vref;
       ++tile;
-      expand(ring + sl * C::HALF_BYTES);
-      fetch(*g, u, true);
+      expand(ring + sl * C::HALF_BYTES, ck);
       publish(&sc.full[sl]);
       ++kv;
+      // what the registers hold next: the following unit, of this segment or of the next one
+      const Segment *f = g;
+      int fu = u + 1;
+      if (fu == u1) {
+        rd.done(sc);
+        f = nxt = rd.next_warp(sc, a, ok);
+        if (f) fu = f->u0;
+      }
+      if (f) {
+        fetch(*f, fu, false, ck);
+        fetch_scales(*f, fu);
+      }
       sl = kv % C::NSLOT;
       if (!wait(&sc.empty[sl], ((kv / C::NSLOT) & 1) ^ 1)) break;
-      expand(ring + sl * C::HALF_BYTES);
-      if (u + 1 < u1) {
-        fetch(*g, u + 1, false);
-        fetch_scales(*g, u + 1);
-      } else {
-        rd.done(sc);
-        nxt = rd.next_warp(sc, a, ok);
-        if (nxt) {
-          fetch(*nxt, nxt->u0, false);
-          fetch_scales(*nxt, nxt->u0);
-        }
-      }
+      expand(ring + sl * C::HALF_BYTES, cv);
       publish(&sc.full[sl]);
       ++kv;
+      if (f) fetch(*f, fu, true, cv);
     }
     if (!ok) break;
     g = nxt;
@@ -450,6 +479,10 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
 
 // ------------------------------------------------------------------ MMA issuers
 
+// Groups of one half: S(0) and S(1), then P V(j) with S(j + 2) behind it. Halves alternate group by group.
+// The whole warp walks through the loop and one lane issues: descriptors then live in uniform registers,
+// where a lone thread pays several moves for each of them (measured: 80 cycles an instruction under the
+// softmax warps' load, of which the tensor core needs 32 to 64).
 template <class C>
 __device__ void tile_mma(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint8_t *q_smem, uint8_t *ring, int w) {
   const volatile int *ab = &sc.abort_flag;
@@ -458,79 +491,91 @@ __device__ void tile_mma(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint
   const uint64_t k_desc0 = smem_desc_sw128(smem_u32(ring), 16, 1024);
   const uint64_t v_desc0 = smem_desc_sw128(smem_u32(ring), 128 * 128, 1024);
   constexpr uint32_t kUnits = C::HALF_BYTES / 16;
-  const uint32_t s_tmem = tmem + w * C::COLS, o_tmem = s_tmem + 128;
-  uint32_t kv = 0, qi = 0, p_ph = 0, g = 0, o_ph = 0;
+  constexpr uint32_t kStepUnits = kStepKeys * 128 / 16;  // from one step's keys to the next in a unit
+  const uint32_t o_tmem = tmem + w * C::COLS, s_tmem = o_tmem + C::D;
+  uint32_t kv = 0, qi = 0, p_ph = 0, g = 0, o_ph = 0;  // p_ph: bit b is the phase of buffer b
   bool ok = true;
+  const uint32_t lead = elect_one();
   auto wait = [&](uint64_t *bar, uint32_t par) {
-    if (!ok) return false;
-    if (!mbar_wait(bar, par, a.timeout_ns, ab)) ok = false;
-    else tc_fence_after_sync();
+    ok = __all_sync(0xffffffffu, mbar_wait(bar, par, a.timeout_ns, ab));
+    tc_fence_after_sync();
     return ok;
   };
   auto take = [&](uint32_t target) {
-    if (*turn == target) return true;
+    if (__all_sync(0xffffffffu, *turn == target)) return true;
     const uint64_t t0 = global_timer_ns();
     for (uint32_t it = 1;; ++it) {
-      if (*turn == target) return true;
-      if ((it & 255u) == 0u && (*ab || global_timer_ns() - t0 > a.timeout_ns)) {
+      if (__all_sync(0xffffffffu, *turn == target)) return true;
+      if ((it & 255u) == 0u && __any_sync(0xffffffffu, *ab || global_timer_ns() - t0 > a.timeout_ns)) {
         ok = false;
         return false;
       }
     }
   };
+  auto pass = [&](uint32_t next) {
+    if (lead) *turn = next;
+    __syncwarp();
+  };
   SegmentReader<C> rd;
-  while (const Segment *sg = ok ? rd.next(sc, a, ok) : nullptr) {
-    const int n = sg->n, klim = sg->klim, u0 = sg->u0;
-    rd.done(sc);
+  while (const Segment *sg = ok ? rd.next_warp(sc, a, ok) : nullptr) {
+    // (a broadcast tells the compiler that the values are the same in every lane)
+    const int n = __shfl_sync(0xffffffffu, sg->n, 0), ns = __shfl_sync(0xffffffffu, sg->ns, 0);
+    const int klim = __shfl_sync(0xffffffffu, sg->klim, 0), base = __shfl_sync(0xffffffffu, sg->u0, 0) * kUnitKeys;
+    __syncwarp();
+    if (lead) rd.done(sc);
     const uint32_t qe = qi + w;
     qi += 2;
     if (!wait(&sc.q_full[qe % C::NQ], (qe / C::NQ) & 1)) break;
     const uint64_t q_desc = q_desc0 + (qe % C::NQ) * kUnits;
-    auto issue_qk = [&](int i) {
-      const uint64_t kd = k_desc0 + ((kv + 2 * i) % C::NSLOT) * kUnits;
-      const uint32_t idesc = idesc_16bit_f32(128, 16 * unit_steps(klim, u0 + i), false, C::FP16);
+    auto issue_qk = [&](int j) {
+      const uint64_t kd = k_desc0 + ((kv + (j & ~1)) % C::NSLOT) * kUnits + (j & 1) * kStepUnits;
+      const uint32_t idesc = idesc_16bit_f32(128, 16 * step_slices(klim, base + j * kStepKeys), false, C::FP16);
 #pragma unroll
       for (int kk = 0; kk < C::D / 16; ++kk) {
         const uint64_t off = static_cast<uint64_t>((kk >> 2) * (128 * 128 / 16) + (kk & 3) * 2);
-        mma_bf16_ss(s_tmem, q_desc + off, kd + off, idesc, kk > 0 ? 1u : 0u);
+        mma_ss_if(lead, s_tmem + (j & 1) * kStepKeys, q_desc + off, kd + off, idesc, kk > 0 ? 1u : 0u);
       }
-      tc_commit(&sc.s_full[w]);
     };
     auto wait_entry = [&](uint32_t e) { return wait(&sc.full[e % C::NSLOT], (e / C::NSLOT) & 1); };
     if (!wait_entry(kv) || !take(g + w)) break;
     issue_qk(0);
-    *turn = g + w + 1;
-    for (int i = 0; i < n && ok; ++i) {
-      if (!wait_entry(kv + 2 * i + 1)) break;
-      if (i + 1 < n && !wait_entry(kv + 2 * i + 2)) break;
-      if (i == 0 && !wait(&sc.o_empty[w], o_ph ^ 1)) break;
-      if (!wait(&sc.p_full[w], p_ph)) break;
-      p_ph ^= 1;
-      const uint32_t my = g + 2 + 2 * i + w;
-      if (!take(my)) break;
-      const uint64_t vd = v_desc0 + ((kv + 2 * i + 1) % C::NSLOT) * kUnits;
-      const int steps = unit_steps(klim, u0 + i);
-      if (steps == 8) {
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          mma_bf16_ts(o_tmem, s_tmem + kk * 8, vd + static_cast<uint64_t>(kk * (16 * 128 / 16)), C::IDESC_PV, (i > 0 || kk > 0) ? 1u : 0u);
-      } else {
-        for (int kk = 0; kk < steps; ++kk)
-          mma_bf16_ts(o_tmem, s_tmem + kk * 8, vd + static_cast<uint64_t>(kk * (16 * 128 / 16)), C::IDESC_PV, (i > 0 || kk > 0) ? 1u : 0u);
+    tc_commit_if(lead, &sc.s_full[w][0]);
+    if (ns > 1) {
+      issue_qk(1);
+      tc_commit_if(lead, &sc.s_full[w][1]);
+    }
+    pass(g + w + 1);
+    for (int j = 0; j < ns && ok; ++j) {
+      const int b = j & 1;
+      if (b == 0) {
+        if (!wait_entry(kv + j + 1)) break;                    // V of the step's unit
+        if (j + 2 < ns && !wait_entry(kv + j + 2)) break;      // K of the next unit
       }
-      if (i + 1 < n) issue_qk(i + 1);
-      else tc_commit(&sc.o_full[w]);
-      *turn = my + 1;
+      if (j == 0 && !wait(&sc.o_empty[w], o_ph ^ 1)) break;
+      if (!wait(&sc.p_full[w][b], (p_ph >> b) & 1)) break;
+      p_ph ^= 1u << b;
+      const uint32_t my = g + 2 + 2 * j + w;
+      if (!take(my)) break;
+      const uint64_t vd = v_desc0 + ((kv + (j & ~1) + 1) % C::NSLOT) * kUnits + b * kStepUnits;
+      const uint32_t p_tmem = s_tmem + b * kStepKeys;
+      const int slices = step_slices(klim, base + j * kStepKeys);
+#pragma unroll
+      for (int kk = 0; kk < 4; ++kk)
+        if (kk < slices)
+          mma_ts_if(lead, o_tmem, p_tmem + kk * 8, vd + static_cast<uint64_t>(kk * (16 * 128 / 16)), C::IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
+      pass(my + 1);  // the other issuer wakes while this one is still at S(j + 2)
+      if (j + 2 < ns) issue_qk(j + 2);
+      tc_commit_if(lead, &sc.s_full[w][b]);  // S(j + 2), or the end of P V(j)
     }
     if (!ok) break;
     o_ph ^= 1;
     kv += 2 * n;
-    g += 2 + 2 * n;
+    g += 2 + 2 * ns;
   }
-  if (!ok) tile_abort(&sc.abort_flag, a.status);
+  if (!ok && lead) tile_abort(&sc.abort_flag, a.status);
   // Every tcgen05 operation issued here must finish before TMEM is released.
   const int zero = 0;
-  tc_commit(&sc.mma_done[w]);
+  tc_commit_if(lead, &sc.mma_done[w]);
   mbar_wait(&sc.mma_done[w], 0, a.timeout_ns, &zero);
 }
 
@@ -544,11 +589,10 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
   using MT = typename C::MT;
   const volatile int *ab = &sc.abort_flag;
   const int wq = warp & 3, row = wq * 32 + lane;
-  const uint32_t s_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16) + w * C::COLS;
-  const uint32_t o_addr = s_addr + 128;
+  const uint32_t o_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16) + w * C::COLS;
   const bool leader = (threadIdx.x & 127) == 0;
   const uint64_t pol_out = l2_policy_evict_first();
-  uint32_t kv = 0, qi = 0, tile = 0, s_ph = 0, o_ph = 0;
+  uint32_t kv = 0, qi = 0, tile = 0, s_ph = 0;  // s_ph: bit b is the phase of S buffer b
   bool ok = true;
   auto wait = [&](uint64_t *bar, uint32_t par) {
     bool x = mbar_wait(bar, par, a.timeout_ns, ab);
@@ -560,7 +604,7 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
   auto release = [&](uint32_t e) { mbar_arrive(&sc.empty[e % C::NSLOT]); };
   SegmentReader<C> rd;
   while (const Segment *sg = ok ? rd.next_warp(sc, a, ok) : nullptr) {
-    const int n = sg->n;
+    const int n = sg->n, ns = sg->ns;
     int lim;
     {
       int tok, hg;
@@ -569,159 +613,115 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
     }
     const uint32_t qe = qi + w;
     qi += 2;
-    float m_ref = -CUDART_INF_F, l = 0.f, vref = 0.f, down = 1.f;
-    for (int i = 0; i < n; ++i, ++tile) {
-      if (!wait(&sc.s_full[w], s_ph)) break;
-      s_ph ^= 1;
+    float m_ref = -CUDART_INF_F, l = 0.f, vref = 0.f;
+    for (int j = 0; j < ns; ++j) {
+      const int b = j & 1;
+      if (!wait(&sc.s_full[w][b], (s_ph >> b) & 1)) break;
+      s_ph ^= 1u << b;
       if constexpr (C::BITS8) {  // the converter's scales (complete: the product above used the same buffers)
-        const uint32_t ke = kv + 2 * i;
+        const uint32_t ke = kv + (j & ~1);
         if (!wait(&sc.full[ke % C::NSLOT], (ke / C::NSLOT) & 1)) break;
-        if (i == 0) {
-          if (!wait(&sc.q_full[qe % C::NQ], (qe / C::NQ) & 1)) break;
-          down = sc.qdown[qe % C::NQ][row];
-        }
       }
-      // The group that produced this S is complete: K of this unit and V of the one before have
-      // been read by this half, and after the last S its queries.
+      // The group that produced this S is complete, so this half has done with K of the unit (after its
+      // last step), with V of the unit that ended two steps ago, and after the last S with its queries.
       if (leader) {
-        release(kv + 2 * i);
-        if (i > 0) release(kv + 2 * i - 1);
+        if (b == 1 || j == ns - 1) release(kv + (j & ~1));
+        if (b == 1 && j >= 3) release(kv + j - 2);
       }
       // (a complete tile keeps its queries' buffer for its output)
-      if (i == n - 1 && sg->part >= 0 && lane == 0) mbar_arrive(&sc.q_empty[qe % C::NQ]);
-      const int base = (sg->u0 + i) * kUnitKeys, klim = sg->klim;
-      const int left = lim - base;  // keys of this unit that the row sees
-      const bool plain = __all_sync(0xffffffffu, left >= kUnitKeys);
-      const int nch = (16 * unit_steps(klim, sg->u0 + i) + 31) >> 5;  // 32-column chunks in use
+      if (j == ns - 1 && sg->part >= 0 && lane == 0) mbar_arrive(&sc.q_empty[qe % C::NQ]);
+      const int base = sg->u0 * kUnitKeys + j * kStepKeys;
+      const int left = lim - base;  // keys of this step that the row sees
+      const bool plain = __all_sync(0xffffffffu, left >= kStepKeys);
+      const uint32_t s_addr = o_addr + D + b * kStepKeys;
       float alpha = 1.f, lsum = 0.f;
-      const int ss = tile % C::NSC;
-      // Exponentials of one 32-column chunk (v: scores) against -neg_m, to P; row sums into acc.
-      auto exp_chunk = [&](const uint32_t *v, int c, uint64_t scp, uint64_t nmp, uint64_t(&acc)[4], auto poly_tag) {
-        constexpr bool POLY = decltype(poly_tag)::value;
+      const float *kscale = C::BITS8 ? &sc.ks[(tile + (j >> 1)) % C::NSC][b * kStepKeys] : nullptr;
+      const float *vscale = C::BITS8 ? &sc.vs[(tile + (j >> 1)) % C::NSC][b * kStepKeys] : nullptr;
+      uint32_t x[kStepKeys];
+      // P = 2^(x f - m) of 32-column chunk c; f: the logit scale, a key's own scale, or 1 (PRE: x is
+      // scaled already). POLY: some pairs on the FMA pipe.
+      auto exp_chunk = [&](int c, float neg_m, uint64_t(&acc)[2], auto poly_tag, auto pre_tag) {
+        constexpr bool POLY = decltype(poly_tag)::value, PRE = decltype(pre_tag)::value;
+        const uint64_t nmp = f2(neg_m, neg_m);
         uint32_t pk[16];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const uint64_t xx = fma2(f2(u2f_(v[2 * e]), u2f_(v[2 * e + 1])), scp, nmp);
-          float x0, x1, p0, p1;
-          f2_split(xx, x0, x1);
-          if (POLY && ((kTilePolyMask >> (e % 8)) & 1u)) {
-            exp2_poly_nan_x2(x0, x1, p0, p1);
-          } else {
-            p0 = ex2_approx(x0);
-            p1 = ex2_approx(x1);
+        for (int e = 0; e < 16; e += 2) {
+          [[maybe_unused]] float4 kk, vv;
+          if constexpr (C::BITS8 && !PRE) kk = *reinterpret_cast<const float4 *>(kscale + c * 32 + 2 * e);
+          if constexpr (C::BITS8) vv = *reinterpret_cast<const float4 *>(vscale + c * 32 + 2 * e);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            const uint64_t v = f2(u2f_(x[c * 32 + 2 * (e + t)]), u2f_(x[c * 32 + 2 * (e + t) + 1]));
+            uint64_t xx;
+            if constexpr (PRE) xx = add2(v, nmp);
+            else if constexpr (C::BITS8) xx = fma2(v, t ? f2(kk.z, kk.w) : f2(kk.x, kk.y), nmp);
+            else xx = fma2(v, f2(a.scale_log2, a.scale_log2), nmp);
+            float x0, x1, p0, p1;
+            f2_split(xx, x0, x1);
+            if (POLY && ((kTilePolyMask >> ((e + t) % 8)) & 1u)) {
+              exp2_poly_nan_x2(x0, x1, p0, p1);
+            } else {
+              p0 = ex2_approx(x0);
+              p1 = ex2_approx(x1);
+            }
+            acc[t] = add2(acc[t], f2(p0, p1));
+            if constexpr (C::BITS8) {
+              p0 *= t ? vv.z : vv.x;
+              p1 *= t ? vv.w : vv.y;
+            }
+            pk[e + t] = pack16<MT>(p0, p1);
           }
-          acc[e & 3] = add2(acc[e & 3], f2(p0, p1));
-          if constexpr (C::BITS8) {
-            const float2 vv = *reinterpret_cast<const float2 *>(&sc.vs[ss][c * 32 + 2 * e]);
-            p0 *= vv.x, p1 *= vv.y;
-          }
-          pk[e] = pack16<MT>(p0, p1);
         }
         tmem_st16(s_addr + c * 16, pk);
       };
-      auto total = [&](const uint64_t(&acc)[4]) {
-        float t0, t1, t2, t3, t4, t5, t6, t7;
+      auto total = [&](const uint64_t(&acc)[2]) {
+        float t0, t1, t2, t3;
         f2_split(acc[0], t0, t1);
         f2_split(acc[1], t2, t3);
-        f2_split(acc[2], t4, t5);
-        f2_split(acc[3], t6, t7);
-        return ((t0 + t1) + (t2 + t3)) + ((t4 + t5) + (t6 + t7));
+        return (t0 + t1) + (t2 + t3);
       };
-      if constexpr (!C::BITS8) {
-        // The row in registers: P overwrites S, and a unit may have to be done again.
-        uint32_t x[128];
-        auto run = [&](auto full_tag) {
-          constexpr bool FULL = decltype(full_tag)::value;  // all four chunks, no masks
-          auto exp_all = [&](float neg_m, auto poly_tag) {
-            const uint64_t scp = f2(a.scale_log2, a.scale_log2), nmp = f2(neg_m, neg_m);
-            uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
+      tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(x));
+      tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
+      tmem_wait_ld();
+      reg_fence<kStepKeys>(x);
+      bool done = false;
+      if (plain && __all_sync(0xffffffffu, m_ref != -CUDART_INF_F)) {
+        uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-            for (int c = 0; c < 4; ++c)
-              if (FULL || c < nch) exp_chunk(x + c * 32, c, scp, nmp, acc, poly_tag);
-            return total(acc);
-          };
+        for (int c = 0; c < 2; ++c) exp_chunk(c, -m_ref, acc, std::true_type{}, std::false_type{});
+        lsum = total(acc);
+        done = __all_sync(0xffffffffu, lsum <= kTileSumLimit);
+        if (!done) tmem_wait_st();
+      }
+      if (!done) {
+        // With the row maximum: a row's first step, masked steps, and large values.
 #pragma unroll
-          for (int c = 0; c < 4; ++c)
-            if (FULL || c < nch) tmem_ld32(s_addr + c * 32, *reinterpret_cast<uint32_t(*)[32]>(x + c * 32));
-          tmem_wait_ld();
-          reg_fence<128>(x);
-          if (!FULL) {
-#pragma unroll
-            for (int e = 0; e < 128; ++e)
-              if (e >= left) x[e] = __float_as_uint(-CUDART_INF_F);
-          }
-          if (__all_sync(0xffffffffu, m_ref != -CUDART_INF_F)) {
-            lsum = exp_all(-m_ref, std::true_type{});
-            if (__all_sync(0xffffffffu, lsum <= kTileSumLimit)) return;
-            tmem_wait_st();
-          }
-          const float mx = max_tree_bits<128>(x) * a.scale_log2;
-          if (mx > m_ref + kTileSlack) {
-            if (m_ref != -CUDART_INF_F) alpha = ex2_approx(m_ref - mx);
-            m_ref = mx;
-          }
-          lsum = exp_all(m_ref == -CUDART_INF_F ? 0.f : -m_ref, std::false_type{});
-        };
-        if (plain) run(std::true_type{});
-        else run(std::false_type{});
-      } else {
-        // The scales leave no room for the row: it is read twice, a chunk at a time, for its maximum
-        // (NaN wins and takes the row) and for the exponentials. P of chunk c overwrites columns of
-        // chunk c / 2, which has been read.
-        auto load = [&](int c, uint32_t(&v)[32]) {
-          tmem_ld32(s_addr + c * 32, v);
-          tmem_wait_ld();
-          reg_fence32(v);
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float4 kk = *reinterpret_cast<const float4 *>(&sc.ks[ss][c * 32 + e]);
-            v[e] = __float_as_uint(u2f_(v[e]) * kk.x);
-            v[e + 1] = __float_as_uint(u2f_(v[e + 1]) * kk.y);
-            v[e + 2] = __float_as_uint(u2f_(v[e + 2]) * kk.z);
-            v[e + 3] = __float_as_uint(u2f_(v[e + 3]) * kk.w);
-          }
-          if (!plain) {
-#pragma unroll
-            for (int e = 0; e < 32; ++e)
-              if (c * 32 + e >= left) v[e] = __float_as_uint(-CUDART_INF_F);
-          }
-        };
-        float mx = -CUDART_INF_F;
-#pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
-          uint32_t v[32];
-          load(c, v);
-          float m0 = mx, m1 = mx;
-#pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            m0 = fmax3_nan(m0, u2f_(v[e]), u2f_(v[e + 1]));
-            m1 = fmax3_nan(m1, u2f_(v[e + 2]), u2f_(v[e + 3]));
-          }
-          mx = fmax3_nan(mx, m0, m1);
+        for (int e = 0; e < kStepKeys; ++e) {
+          float f = a.scale_log2;
+          if constexpr (C::BITS8) f = kscale[e];
+          x[e] = e < left ? __float_as_uint(u2f_(x[e]) * f) : __float_as_uint(-CUDART_INF_F);
         }
-        mx *= down;
-        if (!(mx <= m_ref + kTileSlack)) {
+        const float mx = max_tree_bits<kStepKeys>(x);
+        if (mx > m_ref + kTileSlack) {
           if (m_ref != -CUDART_INF_F) alpha = ex2_approx(m_ref - mx);
           m_ref = mx;
         }
-        const float neg_m = m_ref == -CUDART_INF_F ? 0.f : -m_ref;
-        const uint64_t scp = f2(down, down), nmp = f2(neg_m, neg_m);
-        uint64_t acc[4] = {f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f), f2(0.f, 0.f)};
-#pragma unroll 1
-        for (int c = 0; c < nch; ++c) {
-          uint32_t v[32];
-          load(c, v);
-          exp_chunk(v, c, scp, nmp, acc, std::true_type{});
-        }
+        uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 2; ++c)
+          exp_chunk(c, m_ref == -CUDART_INF_F ? 0.f : -m_ref, acc, std::false_type{}, std::true_type{});
         lsum = total(acc);
       }
       l = l * alpha + lsum;
       if constexpr (C::BITS8) {
-        alpha *= sc.vgrow[ss];
-        vref = sc.vref[ss];
+        if (b == 0) {
+          alpha *= sc.vgrow[(tile + (j >> 1)) % C::NSC];
+          vref = sc.vref[(tile + (j >> 1)) % C::NSC];
+        }
       }
-      if (i > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        // P V of the unit before has completed (its commit was this S's), so O can be rescaled.
+      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+        // O is at rest once P V of the step before has completed: the other buffer's next commit.
+        if (!wait(&sc.s_full[w][b ^ 1], (s_ph >> (b ^ 1)) & 1)) break;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -733,12 +733,12 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
           tmem_st32(o_addr + c * 32, o);
         }
       }
-      if (!C::BITS8 && i == n - 1 && unit_ragged(sg->L, klim, sg->u0 + i)) {
-        // both halves write the same zeros, each before its own product
-        const uint32_t ve = kv + 2 * i + 1;
+      if (!C::BITS8 && j == ns - 1 && sg->L < base + 16 * step_slices(sg->klim, base)) {
+        // The sequence ends inside this step. Both halves write the same zeros, each before its own product.
+        const uint32_t ve = kv + (j & ~1) + 1;
         if (!wait(&sc.full[ve % C::NSLOT], (ve / C::NSLOT) & 1)) break;
-        uint8_t *v = ring + (ve % C::NSLOT) * C::HALF_BYTES;
-        const int r0 = max(sg->L - base, 0), r1 = 16 * unit_steps(klim, sg->u0 + i);
+        uint8_t *v = ring + (ve % C::NSLOT) * C::HALF_BYTES + b * (kStepKeys * 128);
+        const int r0 = max(sg->L - base, 0), r1 = 16 * step_slices(sg->klim, base);
         for (int e = row; e < (r1 - r0) * 8 * C::PANELS; e += 128) {
           const int r = r0 + e / (8 * C::PANELS), ch = e % (8 * C::PANELS);
           *reinterpret_cast<uint4 *>(v + (ch >> 3) * (128 * 128) + r * 128 + (ch & 7) * 16) = make_uint4(0, 0, 0, 0);
@@ -747,13 +747,22 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
       }
       tmem_wait_st();
       tc_fence_before_sync();
-      mbar_arrive(&sc.p_full[w]);
+      mbar_arrive(&sc.p_full[w][b]);
     }
     if (!ok) break;
-    // ---- the last P V of this half is done: write its rows
-    if (!wait(&sc.o_full[w], o_ph)) break;
-    o_ph ^= 1;
-    if (leader) release(kv + 2 * n - 1);
+    tile += n;
+    // ---- the last two P V of this half are done: write its rows
+    if (ns > 1) {
+      if (!wait(&sc.s_full[w][ns & 1], (s_ph >> (ns & 1)) & 1)) break;
+      s_ph ^= 1u << (ns & 1);
+    }
+    if (!wait(&sc.s_full[w][(ns - 1) & 1], (s_ph >> ((ns - 1) & 1)) & 1)) break;
+    s_ph ^= 1u << ((ns - 1) & 1);
+    if (leader) {
+      // values not returned yet: the steps released those of units before (last odd step - 1) / 2
+      const int last = (ns - 1) & 1 ? ns - 1 : ns - 2;  // last odd step, or -1
+      for (int i = last >= 3 ? (last - 1) / 2 : 0; i < n; ++i) release(kv + 2 * i + 1);
+    }
     kv += 2 * n;
     const float vm = C::BITS8 ? vref : 1.f;
     if (sg->part >= 0) {
@@ -849,9 +858,10 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       mbar_init(&sc.q_empty[i], 4);  // the half's softmax warps
     }
     for (int w = 0; w < 2; ++w) {
-      mbar_init(&sc.s_full[w], 1);
-      mbar_init(&sc.p_full[w], 128);
-      mbar_init(&sc.o_full[w], 1);
+      for (int b = 0; b < 2; ++b) {
+        mbar_init(&sc.s_full[w][b], 1);
+        mbar_init(&sc.p_full[w][b], 128);
+      }
       mbar_init(&sc.o_empty[w], 128);
       mbar_init(&sc.mma_done[w], 1);
     }
@@ -889,7 +899,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   const uint32_t tmem = sc.tmem_base;
   if (warp < 4) regs_dec<C::CTRL_REGS>();
   else if (warp < 12) regs_inc<C::SOFTMAX_REGS>();
-  else if constexpr (C::BITS8) regs_dec<C::CONV_REGS>();
+  else if constexpr (C::BITS8) regs_inc<C::CONV_REGS>();
   if (warp < 4) {
     if (warp == 0) {
       if constexpr (!C::BITS8) {
@@ -897,7 +907,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
     } else if (warp == 2) {
       tile_scheduler<C>(sc, a, x, lane);
-    } else if (lane == 0) {
+    } else {
       tile_mma<C>(sc, a, tmem, q_smem, ring, warp == 1 ? 0 : 1);
     }
   } else if (warp < 12) {
