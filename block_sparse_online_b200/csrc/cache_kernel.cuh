@@ -6,18 +6,24 @@
 // TOP = 127 (int8) or 448 (e4m3, its largest value); a row of zeros has scale 0 and codes 0,
 // a row with an element that is not finite has scale NaN, so all of it reads back as NaN.
 // The code is the one nearest to the exact ratio: x_e TOP is exact in fp32 (11 bits by 7)
-// and a ratio that is no tie lies at least 2^-19 of itself from one, so the correctly
-// rounded fp32 quotient falls on the right side of it. (Dividing by the ROUNDED scale does
-// not: for amax / TOP inexact it turns ties to one side.)
+// and a ratio that is no tie lies at least 2^-19 of itself from one, so an fp32 quotient that
+// is exact for short ratios and near for the others falls on the right side of it: the product
+// with the row's reciprocal (off by 2^-22), corrected once by its residual, is off by 2^-45 before
+// its last rounding. (Dividing by the ROUNDED scale turns ties to one side; a full division
+// for each element cost 14 us where the row's reciprocal and two more products cost 6: 1560 tokens of
+// 12 heads of 128.)
 // Read back: fl16(code_e scale), one rounding.
 //
-// Memory bound: every row is read once and written once. D / 8 lanes hold a row, 8 elements
-// (one 16-byte access of 16-bit data) each, and reduce |x| with shuffles. A block serves
-// `tokens` consecutive tokens over all heads, keys and values; where each of them lives
-// (sequence, page) is found once and kept in shared memory.
+// Memory bound: every row is read once and written once. A block serves 2^k consecutive tokens
+// over all heads, keys and values; where each token lives (sequence, page) is found once and
+// kept in shared memory. Rows go token fastest, so that neighbouring lanes read neighbouring
+// rows of a page, and a row's token, head and kind are shifts and masks of its number. A lane
+// holds pieces of 8 elements (one 16-byte access of 16-bit data): one piece when writing, where the
+// row's maximum takes shuffles and the divisions registers, two when reading.
 #pragma once
 
 #include "dense_common.cuh"
+#include "rows_kernel.cuh"
 
 namespace solattn {
 
@@ -28,7 +34,7 @@ struct CacheArgs {
   void *new_k, *new_v;                                   // 16-bit rows: read (write call) or written (read call)
   long long nk_tok, nk_head, nv_tok, nv_head;
   const int *table, *cu, *len;
-  int width, page, page_shift, num_pages, B, Hkv, total, tokens;
+  int width, page, page_shift, num_pages, B, Hkv, total, token_shift;
   int *status;
 };
 
@@ -52,30 +58,61 @@ __device__ __forceinline__ float max_nan(float a, float b) {
 }
 
 constexpr int kCacheThreads = 256;
-constexpr int kCacheTokens = 32;  // most tokens of a block
+constexpr int kCacheCu = 1024;  // sequence bounds that are searched in shared memory
+// Pieces of 8 elements of a lane, and rows of a block at a time (the most tokens that a block serves).
+template <int D, bool WRITE>
+struct CacheShape {
+  static constexpr int PC = WRITE ? 1 : 2;
+  static constexpr int LPR = D / (8 * PC);
+  static constexpr int RPB = kCacheThreads / LPR;
+  static constexpr int U = WRITE ? 2 : 8;  // rows of a lane in flight (reading a 75600-token cache: 2, 4, 8 rows 248, 253, 240 us)
+};
 
 // WRITE: rows into the pages; else rows out of them.
 template <class QT, int KIND, int D, bool WRITE>
-__global__ void __launch_bounds__(kCacheThreads) cache_kernel(const CacheArgs a) {
-  constexpr int LPR = D / 8;                    // lanes of a row
-  constexpr int RPB = kCacheThreads / LPR;      // rows of a block at a time
-  constexpr int U = 4;                          // rows of a lane in flight
-  __shared__ int s_page[kCacheTokens], s_row[kCacheTokens];
-  const int t0 = blockIdx.x * a.tokens;
-  const int nt = min(a.tokens, a.total - t0);
+__global__ void __launch_bounds__(kCacheThreads) cache_kernel(const __grid_constant__ CacheArgs a) {
+  using C = CacheShape<D, WRITE>;
+  constexpr int PC = C::PC, LPR = C::LPR, U = C::U;
+  __shared__ int s_page[C::RPB], s_row[C::RPB], s_cu[kCacheCu];
+  const int t0 = blockIdx.x << a.token_shift;
+  const int nt = min(1 << a.token_shift, a.total - t0);
+  const int lane = threadIdx.x % LPR, g = threadIdx.x / LPR;
+  // A thread keeps its token; its rows are (head, key or value) pairs hk = hk0 + i * step.
+  const int t = g & ((1 << a.token_shift) - 1);
+  const int hk0 = g >> a.token_shift, step = C::RPB >> a.token_shift, n_hk = 2 * a.Hkv;
+  const bool live = t < nt;
+  QT *new_k = static_cast<QT *>(a.new_k) + static_cast<long long>(t0 + t) * a.nk_tok + lane * 8;
+  QT *new_v = static_cast<QT *>(a.new_v) + static_cast<long long>(t0 + t) * a.nv_tok + lane * 8;
+  auto new_row = [&](int hk) { return (hk & 1) ? new_v + (hk >> 1) * a.nv_head : new_k + (hk >> 1) * a.nk_head; };
+  uint4 x[U][PC];
+  // Source rows of a written turn: their place does not wait for the pages.
+  auto load_rows = [&](int hb) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int hk = hb + hk0 + u * step;
+      x[u][0] = live && hk < n_hk ? *reinterpret_cast<const uint4 *>(new_row(hk)) : make_uint4(0, 0, 0, 0);
+    }
+  };
+  if constexpr (WRITE) load_rows(0);
+  const bool in_smem = a.B < kCacheCu;
+  if (in_smem) {
+    for (int i = threadIdx.x; i <= a.B; i += kCacheThreads) s_cu[i] = __ldg(a.cu + i);
+    __syncthreads();
+  }
   if (static_cast<int>(threadIdx.x) < nt) {
-    const int t = t0 + threadIdx.x;
-    // last sequence that begins at or before t: cu is ascending
+    const int tt = t0 + threadIdx.x;
+    auto cu = [&](int i) { return in_smem ? s_cu[i] : __ldg(a.cu + i); };
+    // last sequence that begins at or before the token: cu is ascending
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
-      if (__ldg(a.cu + mid) <= t) lo = mid;
+      if (cu(mid) <= tt) lo = mid;
       else hi = mid;
     }
-    const int end = __ldg(a.cu + lo + 1);
+    const int end = cu(lo + 1);
     int page = -1, row = 0;
-    if (t >= __ldg(a.cu + lo) && t < end) {  // rows in front of the first and behind the last sequence are left alone
-      const int pos = __ldg(a.len + lo) - (end - t);
+    if (tt >= cu(lo) && tt < end) {  // rows in front of the first and behind the last sequence are left alone
+      const int pos = __ldg(a.len + lo) - (end - tt);
       bool ok = pos >= 0 && (pos >> a.page_shift) < a.width;
       if (ok) {
         page = __ldg(a.table + static_cast<size_t>(lo) * a.width + (pos >> a.page_shift));
@@ -91,62 +128,33 @@ __global__ void __launch_bounds__(kCacheThreads) cache_kernel(const CacheArgs a)
     s_row[threadIdx.x] = row;
   }
   __syncthreads();
-  const int lane = threadIdx.x % LPR;
-  const int rows = nt * a.Hkv * 2;  // (token, head, key or value), value fastest
-  for (int base = 0; base < rows; base += RPB * U) {
-    const int i0 = base + threadIdx.x / LPR;
-    uint4 x[U];
-    uint2 cd[U];
-    float sc[U];
-    // Every lane of a warp runs every turn (the maxima use whole-warp shuffles).
+  const int page = live ? s_page[t] : -1;
+  const int prow = page >= 0 ? s_row[t] : 0;
+  constexpr int ES = KIND == kKind16 ? 2 : 1;
+  uint8_t *k_row = static_cast<uint8_t *>(a.k) + (max(page, 0) * a.k_seq + prow * a.k_row + lane * 8) * ES;
+  uint8_t *v_row = static_cast<uint8_t *>(a.v) + (max(page, 0) * a.v_seq + prow * a.v_row + lane * 8) * ES;
+  const long long sc_row = static_cast<long long>(max(page, 0)) * a.Hkv * a.page + prow;
+  auto page_row = [&](int hk) { return (hk & 1) ? v_row + (hk >> 1) * a.v_head * ES : k_row + (hk >> 1) * a.k_head * ES; };
+  auto scale_at = [&](int hk) { return ((hk & 1) ? a.v_scale : a.k_scale) + sc_row + (hk >> 1) * a.page; };
+  // Every lane of a warp runs every turn (the maxima use whole-warp shuffles).
+  for (int hb = 0; hb < n_hk; hb += step * U) {
+    if constexpr (WRITE) {
+      if (hb > 0) load_rows(hb);
 #pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * RPB;
-      const int kv = i & 1, ht = i >> 1, t = min(ht / a.Hkv, nt - 1), h = ht % a.Hkv;
-      const int page = i < rows ? s_page[t] : -1;
-      x[u] = make_uint4(0, 0, 0, 0);
-      cd[u] = make_uint2(0, 0);
-      sc[u] = 0.f;
-      if (page >= 0) {
-        if constexpr (WRITE) {
-          const QT *src = static_cast<const QT *>(kv ? a.new_v : a.new_k) +
-                          static_cast<long long>(t0 + t) * (kv ? a.nv_tok : a.nk_tok) + h * (kv ? a.nv_head : a.nk_head);
-          x[u] = *reinterpret_cast<const uint4 *>(src + lane * 8);
-        } else {
-          const long long at = page * (kv ? a.v_seq : a.k_seq) + h * (kv ? a.v_head : a.k_head) +
-                               s_row[t] * (kv ? a.v_row : a.k_row) + lane * 8;
-          if constexpr (KIND == kKind16) {
-            x[u] = *reinterpret_cast<const uint4 *>(static_cast<const QT *>(kv ? a.v : a.k) + at);
-          } else {
-            cd[u] = *reinterpret_cast<const uint2 *>(static_cast<const uint8_t *>(kv ? a.v : a.k) + at);
-            sc[u] = (kv ? a.v_scale : a.k_scale)[(static_cast<size_t>(page) * a.Hkv + h) * a.page + s_row[t]];
-          }
-        }
-      }
-    }
-#pragma unroll
-    for (int u = 0; u < U; ++u) {
-      const int i = i0 + u * RPB;
-      const int kv = i & 1, ht = i >> 1, t = min(ht / a.Hkv, nt - 1), h = ht % a.Hkv;
-      const int page = i < rows ? s_page[t] : -1;
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-      if constexpr (WRITE) {
-        const long long at = page * (kv ? a.v_seq : a.k_seq) + h * (kv ? a.v_head : a.k_head) +
-                             s_row[t] * (kv ? a.v_row : a.k_row) + lane * 8;
+      for (int u = 0; u < U; ++u) {
+        const int hk = hb + hk0 + u * step;
+        const bool ok = page >= 0 && hk < n_hk;
         if constexpr (KIND == kKind16) {
-          if (page >= 0) *reinterpret_cast<uint4 *>(static_cast<QT *>(kv ? a.v : a.k) + at) = x[u];
+          if (ok) *reinterpret_cast<uint4 *>(page_row(hk)) = x[u][0];
         } else {
+          const uint32_t w[4] = {x[u][0].x, x[u][0].y, x[u][0].z, x[u][0].w};
           constexpr float TOP = KIND == kKindInt8 ? 127.f : 448.f;
-          float y[8], amax = 0.f;
+          float amax = 0.f;
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            y[e] = to_float<QT>(w[e >> 1], e & 1);
-            amax = max_nan(amax, fabsf(y[e]));
-          }
+          for (int e = 0; e < 8; ++e) amax = max_nan(amax, fabsf(to_float<QT>(w[e >> 1], e & 1)));
 #pragma unroll
           for (int o = LPR / 2; o; o >>= 1) amax = max_nan(amax, __shfl_xor_sync(0xffffffffu, amax, o));
           const bool finite = amax < CUDART_INF_F;  // false for NaN
-          float scale = finite ? __fdiv_rn(amax, TOP) : CUDART_NAN_F;
           // x TOP and the quotient keep clear of overflow and of subnormals: rows of very
           // large or very small elements are moved by a power of two first (exact, or below
           // half a code: elements that it flushes are under 2^-20 of the largest)
@@ -154,10 +162,15 @@ __global__ void __launch_bounds__(kCacheThreads) cache_kernel(const CacheArgs a)
           if (amax > 0x1p100f) mul = TOP * 0x1p-30f, den = amax * 0x1p-30f;
           if (amax < 0x1p-100f) mul = TOP * 0x1p60f, den = amax * 0x1p60f;
           if (!finite || amax == 0.f) mul = 0.f, den = 1.f;
+          const float inv = __frcp_rn(den);
+          auto quotient = [&](float y) {
+            const float num = y * mul, q = num * inv;
+            return finite ? fmaf(fmaf(-q, den, num), inv, q) : 0.f;
+          };
           uint32_t out[2] = {0, 0};
 #pragma unroll
           for (int e = 0; e < 8; e += 2) {
-            float c0 = finite ? __fdiv_rn(y[e] * mul, den) : 0.f, c1 = finite ? __fdiv_rn(y[e + 1] * mul, den) : 0.f;
+            const float c0 = quotient(to_float<QT>(w[e >> 1], 0)), c1 = quotient(to_float<QT>(w[e >> 1], 1));
             uint32_t two;
             if constexpr (KIND == kKindInt8) {
               two = (static_cast<uint32_t>(__float2int_rn(c0)) & 0xffu) | ((static_cast<uint32_t>(__float2int_rn(c1)) & 0xffu) << 8);
@@ -168,32 +181,50 @@ __global__ void __launch_bounds__(kCacheThreads) cache_kernel(const CacheArgs a)
             }
             out[e >> 2] |= two << (16 * ((e >> 1) & 1));
           }
-          if (page >= 0) {
-            *reinterpret_cast<uint2 *>(static_cast<uint8_t *>(kv ? a.v : a.k) + at) = make_uint2(out[0], out[1]);
-            if (lane == 0) (kv ? a.v_scale : a.k_scale)[(static_cast<size_t>(page) * a.Hkv + h) * a.page + s_row[t]] = scale;
+          if (ok) {
+            *reinterpret_cast<uint2 *>(page_row(hk)) = make_uint2(out[0], out[1]);
+            if (lane == 0) *scale_at(hk) = finite ? __fdiv_rn(amax, TOP) : CUDART_NAN_F;
           }
         }
-      } else if (page >= 0) {
-        QT *dst = static_cast<QT *>(kv ? a.new_v : a.new_k) + static_cast<long long>(t0 + t) * (kv ? a.nv_tok : a.nk_tok) +
-                  h * (kv ? a.nv_head : a.nk_head) + lane * 8;
-        uint4 r = x[u];
-        if constexpr (KIND != kKind16) {
-          float y[8];
+      }
+    } else if (page >= 0) {
+      [[maybe_unused]] uint2 cd[U][PC];
+      [[maybe_unused]] float sc[U];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t code = ((e < 4 ? cd[u].x : cd[u].y) >> (8 * (e & 3))) & 0xffu;
-            if constexpr (KIND == kKindInt8) {
-              y[e] = static_cast<float>(static_cast<int>(static_cast<int8_t>(code)));
-            } else {
-              uint32_t h2;
-              asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h2) : "h"(static_cast<uint16_t>(code)));
-              y[e] = to_float<__half>(h2, 0);
-            }
-            y[e] *= sc[u];
+      for (int u = 0; u < U; ++u) {
+        const int hk = hb + hk0 + u * step;
+        if (hk < n_hk) {
+          const uint8_t *src = page_row(hk);
+#pragma unroll
+          for (int c = 0; c < PC; ++c) {
+            if constexpr (KIND == kKind16) x[u][c] = ld_stream16(src + c * (D / PC) * 2);
+            else cd[u][c] = ld_stream8(src + c * (D / PC));
           }
-          r = make_uint4(pack16<QT>(y[0], y[1]), pack16<QT>(y[2], y[3]), pack16<QT>(y[4], y[5]), pack16<QT>(y[6], y[7]));
+          if constexpr (KIND != kKind16) sc[u] = __ldg(scale_at(hk));
         }
-        *reinterpret_cast<uint4 *>(dst) = r;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int hk = hb + hk0 + u * step;
+        if (hk < n_hk) {
+          QT *dst = new_row(hk);
+#pragma unroll
+          for (int c = 0; c < PC; ++c) {
+            uint4 r = x[u][c];
+            if constexpr (KIND != kKind16) {
+              uint32_t o[4];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                // two codes: bytes 0, 1 or 2, 3 of a word
+                const uint32_t word = code_word<KIND>(e < 2 ? cd[u][c].x : cd[u][c].y);
+                const uint32_t h2 = (e & 1) ? codes_f16x2<KIND, 1>(word) : codes_f16x2<KIND, 0>(word);
+                o[e] = pack16<QT>(to_float<__half>(h2, 0) * sc[u], to_float<__half>(h2, 1) * sc[u]);
+              }
+              r = make_uint4(o[0], o[1], o[2], o[3]);
+            }
+            *reinterpret_cast<uint4 *>(dst + c * (D / PC)) = r;
+          }
+        }
       }
     }
   }

@@ -305,12 +305,11 @@ int cache_impl(const solattn_cache *cache, const solattn_view *nk, const solattn
   a.width = s->width, a.page = cache->page, a.page_shift = page_shift(cache->page), a.num_pages = cache->num_pages;
   a.B = s->B, a.Hkv = cache->Hkv, a.total = s->total;
   a.status = reinterpret_cast<int *>(static_cast<uint8_t *>(status) + 4);
-  // Tokens of a block: as many as leave four blocks per SM, at most kCacheTokens.
-  const int want = 4 * di.sms;
-  int tokens = s->total / want;
-  tokens = tokens < 1 ? 1 : tokens > kCacheTokens ? kCacheTokens : tokens;
-  a.tokens = tokens;
-  const int blocks = (s->total + tokens - 1) / tokens;
+  // Tokens of a block: the power of two that leaves four blocks per SM, at most its rows at a time.
+  const int most = cache->d == 128 ? (write ? CacheShape<128, true>::RPB : CacheShape<128, false>::RPB)
+                                   : (write ? CacheShape<64, true>::RPB : CacheShape<64, false>::RPB);
+  while (2 << a.token_shift <= most && (s->total >> (a.token_shift + 1)) >= 4 * di.sms) ++a.token_shift;
+  const int blocks = (s->total + (1 << a.token_shift) - 1) >> a.token_shift;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   NvtxRange r(write ? "solattn cache append" : "solattn cache read");
   bool ok;
