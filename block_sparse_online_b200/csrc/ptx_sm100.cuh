@@ -71,6 +71,30 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity, uint64
   }
 }
 
+// The same with the waiting left to the hardware: the thread sleeps until the phase completes or `hint_ns` pass.
+// (A loop of bare tries reads shared memory every few cycles, and a dozen waiting warps then take a third of
+// the bandwidth that the tensor core's operands need.)
+__device__ __forceinline__ bool mbar_try_wait_for(uint64_t *bar, uint32_t parity, uint32_t hint_ns) {
+  uint32_t ok;
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+      "selp.u32 %0, 1, 0, p;\n\t}"
+      : "=r"(ok)
+      : "r"(smem_u32(bar)), "r"(parity), "r"(hint_ns)
+      : "memory");
+  return ok != 0;
+}
+__device__ __forceinline__ bool mbar_sleep(uint64_t *bar, uint32_t parity, uint64_t limit_ns, const volatile int *abort_flag) {
+  if (mbar_try_wait_for(bar, parity, 20000u)) return true;
+  const uint64_t t0 = global_timer_ns();
+  for (;;) {
+    if (mbar_try_wait_for(bar, parity, 20000u)) return true;
+    if (*abort_flag) return false;
+    if (global_timer_ns() - t0 > limit_ns) return false;
+  }
+}
+
 // ------------------------------------------------------------------ TMA
 
 // 3-D tiled bulk tensor load global -> shared, completion counted in bytes on `bar`.

@@ -12,10 +12,15 @@
 //                other half's softmax runs.
 //   warp 2       owns the TMEM allocation; walks the block's range of the line and publishes its
 //                segments (one tile's run of units) to the other roles, a few ahead.
-//   warps 4-11   softmax, one warpgroup for each half, one row per thread. Where a sequence ends inside a
-//                unit they zero the value rows behind the end, which may hold anything (0 times NaN is NaN).
-//   warps 12-15  8-bit keys only: read codes from the pages, expand them to fp16 into the ring (and the
+//   warps 4-19   softmax, two warpgroups for each half (8-bit keys: warps 4-11, one), one row per thread; the
+//                two take the steps in turn. Where a sequence ends inside a step they zero the value rows
+//                behind the end, which may hold anything (0 times NaN is NaN).
+//   last 4 warps 8-bit keys only: read codes from the pages, expand them to fp16 into the ring (and the
 //                queries, scaled, into their buffers), one unit ahead in registers.
+// Two warpgroups and one reference: the warpgroup of step j + 1 exponentiates while the one of step j still
+// works, and waits for j's word (a barrier for each 32 rows) that the reference stands before it hands over
+// its P; if it moved, the step is done again. So a step may take two steps' time: with one warpgroup
+// a half the softmax was busy for 1680 of 1845 cycles a step, of which the tensor core needs 1280.
 // A step is 64 keys. Each half has two buffers of S (P takes the place of its S): Q K^T of step j + 2
 // follows P V of step j, so while a warpgroup exponentiates step j + 1 the tensor core works on its steps
 // j and j + 2. With one buffer of 128 keys instead, S, softmax and P V formed one chain of 3700 cycles a
@@ -40,7 +45,7 @@ namespace solattn {
 
 constexpr float kTileSlack = 8.0f;         // log2 units the reference may lag a unit's maximum
 constexpr float kTileSumLimit = 32768.0f;  // row sum that shows every value <= 2^15
-constexpr uint32_t kTilePolyMask = 0x80u;  // pairs (mod 8) on the polynomial
+constexpr uint32_t kTilePolyMask = 0x88u;  // pairs (mod 8) on the polynomial
 
 template <class QT_, int KIND_, int D_, bool PAGED_>
 struct TileCfg {
@@ -57,19 +62,24 @@ struct TileCfg {
   static constexpr int NSC = 4;  // units whose scales are kept
   static constexpr int COLS = 128 + D;  // tensor memory columns of a half: O, two buffers of S (and P)
   static constexpr int TMEM_COLS = 512;
-  static constexpr int THREADS = BITS8 ? 512 : 384;
-  // Register shares: within what the block is launched with (384 x 168, 512 x 128).
+  // Warpgroups of a half's softmax. Two take the steps in turn; the 8-bit kernels have registers for one.
+  static constexpr int NP = 1;
+  static constexpr int SOFTMAX_WARPS = 8 * NP;
+  static constexpr int THREADS = 128 + 32 * SOFTMAX_WARPS + (BITS8 ? 128 : 0);
+  // Register shares: within what the block is launched with (640 x 96, 512 x 128).
+  static constexpr int LAUNCH_REGS = BITS8 ? 128 : 168;
   static constexpr int CTRL_REGS = BITS8 ? 72 : 104;
   static constexpr int CONV_REGS = 136;
   static constexpr int SOFTMAX_REGS = BITS8 ? 152 : 200;
-  static_assert(CTRL_REGS < (BITS8 ? 128 : 168) && CONV_REGS > 128 && SOFTMAX_REGS > (BITS8 ? 128 : 168),
+  static_assert(CTRL_REGS < LAUNCH_REGS && (!BITS8 || CONV_REGS > LAUNCH_REGS) && SOFTMAX_REGS > LAUNCH_REGS,
                 "control warps give registers up, the others take them");
-  static_assert(BITS8 ? 128 * CTRL_REGS + 128 * CONV_REGS + 256 * SOFTMAX_REGS <= 512 * 128
-                      : 128 * CTRL_REGS + 256 * SOFTMAX_REGS <= 384 * 168, "register split");
+  static_assert(128 * CTRL_REGS + 32 * SOFTMAX_WARPS * SOFTMAX_REGS + (BITS8 ? 128 * CONV_REGS : 0) <= THREADS * LAUNCH_REGS,
+                "register split");
   static constexpr bool FP16 = std::is_same<MT, __half>::value;
   static constexpr uint32_t IDESC_PV = idesc_16bit_f32(128, D, true, FP16);
 };
 
+constexpr int kStatusTimeoutTile = -4;  // SOLATTN_ETIMEOUT
 constexpr int kStepKeys = 64;  // keys of a step: a unit is two (the last may be one)
 constexpr int kSegs = 4;  // segments published ahead
 
@@ -87,12 +97,17 @@ struct TileCtl {
   uint64_t seg_full[kSegs], seg_empty[kSegs];
   uint64_t full[C::NSLOT], empty[C::NSLOT];
   uint64_t q_full[C::NQ], q_empty[C::NQ];
-  uint64_t s_full[2][2], p_full[2][2], o_empty[2];  // by half, and buffer of S
+  uint64_t s_full[2][2], p_full[2][2];  // by half, and buffer of S
+  uint64_t o_pre[2], o_full[2], o_empty[2];  // the tile's last product but one, its last, and O read
+  uint64_t token[2][4][2];  // [half][32 rows][warpgroup]: the reference of its step stands
+  uint64_t fin[2][4][2];    // the same rows at the end of a tile
   uint64_t conv;  // the converter's four warps
   uint64_t mma_done[2];
   uint32_t turn;
   uint32_t tmem_base;
   int abort_flag;
+  int moved[2][4][2];            // a reference of these rows moved in the warpgroup's last step
+  float xm[C::NP == 2 ? 2 : 1][128], xl[C::NP == 2 ? 2 : 1][128];  // references and sums between the warpgroups of a half
   float wmax[2][4];              // converter: largest value scale per warp
   alignas(16) float ks[C::BITS8 ? C::NSC : 1][C::BITS8 ? 128 : 4];  // key scales (x log2(e) / sqrt d)
   alignas(16) float vs[C::BITS8 ? C::NSC : 1][C::BITS8 ? 128 : 4];  // value scales over the reference
@@ -102,7 +117,7 @@ struct TileCtl {
 
 template <class C>
 constexpr size_t tile_smem_bytes() {
-  return 1024 + static_cast<size_t>(C::NQ + C::NSLOT) * C::HALF_BYTES + sizeof(TileCtl<C>);
+  return static_cast<size_t>(C::NQ + C::NSLOT) * C::HALF_BYTES + sizeof(TileCtl<C>);
 }
 
 __device__ __forceinline__ void tma_load_4d_hint(uint32_t dst, const CUtensorMap *map, uint32_t bar, int c0, int c1,
@@ -124,7 +139,7 @@ __device__ __forceinline__ void tma_load_5d_hint(uint32_t dst, const CUtensorMap
 __device__ __forceinline__ void fence_proxy_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 
 __device__ __forceinline__ void tile_abort(int *abort_flag, int *status) {
-  atomicCAS(status, 0, -4);  // SOLATTN_ETIMEOUT
+  atomicCAS(status, 0, kStatusTimeoutTile);
   *reinterpret_cast<volatile int *>(abort_flag) = 1;
 }
 
@@ -148,7 +163,7 @@ __device__ void tile_scheduler(TileCtl<C> &sc, const DenseArgs &a, const TileArg
   int4 rec = make_int4(0, 0, 0, 0);
   for (uint32_t i = 0;; ++i) {
     const int sl = i % kSegs;
-    if (!mbar_wait(&sc.seg_empty[sl], ((i / kSegs) & 1) ^ 1, a.timeout_ns, &sc.abort_flag)) {
+    if (!mbar_sleep(&sc.seg_empty[sl], ((i / kSegs) & 1) ^ 1, a.timeout_ns, &sc.abort_flag)) {
       tile_abort(&sc.abort_flag, a.status);
       break;
     }
@@ -184,7 +199,7 @@ struct SegmentReader {
   // The next segment, or null at the end (or when a wait gave up: ok is cleared).
   __device__ __forceinline__ const Segment *next(TileCtl<C> &sc, const DenseArgs &a, bool &ok) {
     const int sl = i % kSegs;
-    if (!mbar_wait(&sc.seg_full[sl], (i / kSegs) & 1, a.timeout_ns, &sc.abort_flag)) {
+    if (!mbar_sleep(&sc.seg_full[sl], (i / kSegs) & 1, a.timeout_ns, &sc.abort_flag)) {
       ok = false;
       return nullptr;
     }
@@ -193,7 +208,7 @@ struct SegmentReader {
   }
   __device__ __forceinline__ const Segment *next_warp(TileCtl<C> &sc, const DenseArgs &a, bool &ok) {
     const int sl = i % kSegs;
-    if (!__all_sync(0xffffffffu, mbar_wait(&sc.seg_full[sl], (i / kSegs) & 1, a.timeout_ns, &sc.abort_flag))) {
+    if (!__all_sync(0xffffffffu, mbar_sleep(&sc.seg_full[sl], (i / kSegs) & 1, a.timeout_ns, &sc.abort_flag))) {
       ok = false;
       return nullptr;
     }
@@ -228,7 +243,7 @@ __device__ void tile_producer(TileCtl<C> &sc, const DenseArgs &a, const TileArgs
     rd.done(sc);
     auto load_q = [&](int w) {
       const int sl = qi % C::NQ;
-      if (!mbar_wait(&sc.q_empty[sl], ((qi / C::NQ) & 1) ^ 1, a.timeout_ns, ab)) return false;
+      if (!mbar_sleep(&sc.q_empty[sl], ((qi / C::NQ) & 1) ^ 1, a.timeout_ns, ab)) return false;
       mbar_arrive_expect_tx(&sc.q_full[sl], q_bytes * C::PANELS);
       const int tok = tok0 + w * half;
 #pragma unroll
@@ -240,7 +255,7 @@ __device__ void tile_producer(TileCtl<C> &sc, const DenseArgs &a, const TileArgs
     };
     auto load_kv = [&](int u, bool is_v) {
       const int sl = kv % C::NSLOT;
-      if (!mbar_wait(&sc.empty[sl], ((kv / C::NSLOT) & 1) ^ 1, a.timeout_ns, ab)) return false;
+      if (!mbar_sleep(&sc.empty[sl], ((kv / C::NSLOT) & 1) ^ 1, a.timeout_ns, ab)) return false;
       mbar_arrive_expect_tx(&sc.full[sl], C::HALF_BYTES);
       const CUtensorMap *map = is_v ? tm_v : tm_k;
       uint8_t *dst = ring + sl * C::HALF_BYTES;
@@ -274,9 +289,9 @@ __device__ void tile_producer(TileCtl<C> &sc, const DenseArgs &a, const TileArgs
   // No copy may outlive the block: wait (bounded) for the last fill of every buffer.
   const int zero = 0;
   for (uint32_t f = kv > C::NSLOT ? kv - C::NSLOT : 0; f < kv; ++f)
-    mbar_wait(&sc.full[f % C::NSLOT], (f / C::NSLOT) & 1, a.timeout_ns, &zero);
+    mbar_sleep(&sc.full[f % C::NSLOT], (f / C::NSLOT) & 1, a.timeout_ns, &zero);
   for (uint32_t f = qi > C::NQ ? qi - C::NQ : 0; f < qi; ++f)
-    mbar_wait(&sc.q_full[f % C::NQ], (f / C::NQ) & 1, a.timeout_ns, &zero);
+    mbar_sleep(&sc.q_full[f % C::NQ], (f / C::NQ) & 1, a.timeout_ns, &zero);
 }
 
 // ------------------------------------------------------------------ converter (8-bit keys)
@@ -297,33 +312,39 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
   uint32_t kv = 0, qi = 0, tile = 0, conv_ph = 0;
   bool ok = true;
   auto wait = [&](uint64_t *bar, uint32_t par) {
-    bool w = mbar_wait(bar, par, a.timeout_ns, ab);
+    bool w = mbar_sleep(bar, par, a.timeout_ns, ab);
     w = __all_sync(0xffffffffu, w);
     if (!w) ok = false;
     return w;
   };
   uint4 ck[NP], cv[NP];  // codes of the next unit's keys and values
   float ksc, vsc;
+  // Pages of a unit: lane g holds that of its keys 16 (g % 8) .. + 15 (a page has 16 tokens at least), or -1
+  // behind the sequence's end and for bad entries. Looked up a unit ahead of the codes: a lookup
+  // before each row's load took 2300 cycles for a unit's keys.
+  auto fetch_pages = [&](const Segment &c, int u) {
+    const int j = u * kUnitKeys + (lane & 7) * 16;
+    return j < c.L ? page_of(a, c.b, j) : -1;
+  };
   // Codes of a unit's keys or values into registers.
-  auto fetch = [&](const Segment &c, int u, bool is_v, uint4(&cd)[NP]) {
+  auto fetch = [&](const Segment &c, int u, int pages, bool is_v, uint4(&cd)[NP]) {
     const uint8_t *base = static_cast<const uint8_t *>(is_v ? a.v : a.k) + c.h * (is_v ? a.v_head : a.k_head) + pc * 16;
     const long long row = is_v ? a.v_row : a.k_row, seq = is_v ? a.v_seq : a.k_seq;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int j = u * kUnitKeys + i * RPP + rl;
-      int id = -1;
-      if (j < c.L) id = page_of(a, c.b, j);
-      cd[i] = id >= 0 ? ld_stream16(base + id * seq + (j & (a.page - 1)) * row) : make_uint4(0, 0, 0, 0);
+      const int id = __shfl_sync(0xffffffffu, pages, (i * RPP + rl) >> 4);
+      cd[i] = id >= 0 && j < c.L ? ld_stream16(base + id * seq + (j & (a.page - 1)) * row) : make_uint4(0, 0, 0, 0);
     }
   };
   // The scales of a unit: thread t takes key t.
-  auto fetch_scales = [&](const Segment &c, int u) {
+  auto fetch_scales = [&](const Segment &c, int u, int pages) {
     const int j = u * kUnitKeys + tid;
-    int id = -1;
-    if (j < c.L) id = page_of(a, c.b, j);
+    const int id = __shfl_sync(0xffffffffu, pages, tid >> 4);
+    const bool in = id >= 0 && j < c.L;
     const size_t at = (static_cast<size_t>(max(id, 0)) * a.Hkv + c.h) * a.page + (j & (a.page - 1));
-    ksc = id >= 0 ? __ldg(a.k_scale + at) : 0.f;
-    vsc = id >= 0 ? __ldg(a.v_scale + at) : 0.f;
+    ksc = in ? __ldg(a.k_scale + at) : 0.f;
+    vsc = in ? __ldg(a.v_scale + at) : 0.f;
   };
   auto expand = [&](uint8_t *dst, const uint4(&cd)[NP]) {
 #pragma unroll
@@ -352,9 +373,10 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
   SegmentReader<C> rd;
   const Segment *g = rd.next_warp(sc, a, ok);
   if (g) {
-    fetch(*g, g->u0, false, ck);
-    fetch_scales(*g, g->u0);
-    fetch(*g, g->u0, true, cv);
+    const int pages = fetch_pages(*g, g->u0);
+    fetch(*g, g->u0, pages, false, ck);
+    fetch_scales(*g, g->u0, pages);
+    fetch(*g, g->u0, pages, true, cv);
   }
   while (g) {
     // ---- queries of both halves, a row of each per thread. bf16 queries become fp16 after a division of the
@@ -424,6 +446,15 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
     const Segment *nxt = nullptr;
     const int u1 = g->u0 + g->n;
     for (int u = g->u0; u < u1 && ok; ++u) {
+      // what the registers hold next: the following unit, of this segment or of the next one
+      const Segment *f = g;
+      int fu = u + 1;
+      if (fu == u1) {
+        rd.done(sc);
+        f = nxt = rd.next_warp(sc, a, ok);
+        if (f) fu = f->u0;
+      }
+      const int pages = f ? fetch_pages(*f, fu) : -1;
       int sl = kv % C::NSLOT;
       if (!wait(&sc.empty[sl], ((kv / C::NSLOT) & 1) ^ 1)) break;
       // scales: the reference is a power of two >= the largest value scale so far (2^-100 .. 2^100)
@@ -452,24 +483,16 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
       expand(ring + sl * C::HALF_BYTES, ck);
       publish(&sc.full[sl]);
       ++kv;
-      // what the registers hold next: the following unit, of this segment or of the next one
-      const Segment *f = g;
-      int fu = u + 1;
-      if (fu == u1) {
-        rd.done(sc);
-        f = nxt = rd.next_warp(sc, a, ok);
-        if (f) fu = f->u0;
-      }
       if (f) {
-        fetch(*f, fu, false, ck);
-        fetch_scales(*f, fu);
+        fetch(*f, fu, pages, false, ck);
+        fetch_scales(*f, fu, pages);
       }
       sl = kv % C::NSLOT;
       if (!wait(&sc.empty[sl], ((kv / C::NSLOT) & 1) ^ 1)) break;
       expand(ring + sl * C::HALF_BYTES, cv);
       publish(&sc.full[sl]);
       ++kv;
-      if (f) fetch(*f, fu, true, cv);
+      if (f) fetch(*f, fu, pages, true, cv);
     }
     if (!ok) break;
     g = nxt;
@@ -497,7 +520,7 @@ __device__ void tile_mma(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint
   bool ok = true;
   const uint32_t lead = elect_one();
   auto wait = [&](uint64_t *bar, uint32_t par) {
-    ok = __all_sync(0xffffffffu, mbar_wait(bar, par, a.timeout_ns, ab));
+    ok = __all_sync(0xffffffffu, mbar_sleep(bar, par, a.timeout_ns, ab));
     tc_fence_after_sync();
     return ok;
   };
@@ -565,7 +588,9 @@ __device__ void tile_mma(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint
           mma_ts_if(lead, o_tmem, p_tmem + kk * 8, vd + static_cast<uint64_t>(kk * (16 * 128 / 16)), C::IDESC_PV, (j > 0 || kk > 0) ? 1u : 0u);
       pass(my + 1);  // the other issuer wakes while this one is still at S(j + 2)
       if (j + 2 < ns) issue_qk(j + 2);
-      tc_commit_if(lead, &sc.s_full[w][b]);  // S(j + 2), or the end of P V(j)
+      // S(j + 2), or the end of one of the last two P V. These have barriers of their own: the next tile's S may
+      // follow at once, and a second phase of one barrier could pass before the first is seen.
+      tc_commit_if(lead, j + 2 < ns ? &sc.s_full[w][b] : j + 1 < ns ? &sc.o_pre[w] : &sc.o_full[w]);
     }
     if (!ok) break;
     o_ph ^= 1;
@@ -576,32 +601,38 @@ __device__ void tile_mma(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint
   // Every tcgen05 operation issued here must finish before TMEM is released.
   const int zero = 0;
   tc_commit_if(lead, &sc.mma_done[w]);
-  mbar_wait(&sc.mma_done[w], 0, a.timeout_ns, &zero);
+  mbar_sleep(&sc.mma_done[w], 0, a.timeout_ns, &zero);
 }
 
 // ------------------------------------------------------------------ softmax and epilogue
 
+// w: half of the tile; p: which of its warpgroups (NP = 2: steps p, p + 2, ..., all in S buffer p).
 template <class C>
-__device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint8_t *q_smem, uint8_t *ring, int w, int warp,
-                             int lane) {
-  constexpr int D = C::D;
+__device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint8_t *q_smem, uint8_t *ring, int w, int p,
+                             int warp, int lane) {
+  constexpr int D = C::D, NP = C::NP;
   using QT = typename C::QT;
   using MT = typename C::MT;
   const volatile int *ab = &sc.abort_flag;
   const int wq = warp & 3, row = wq * 32 + lane;
   const uint32_t o_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16) + w * C::COLS;
-  const bool leader = (threadIdx.x & 127) == 0;
+  const bool leader = row == 0;  // of its warpgroup
   const uint64_t pol_out = l2_policy_evict_first();
-  uint32_t kv = 0, qi = 0, tile = 0, s_ph = 0;  // s_ph: bit b is the phase of S buffer b
+  uint32_t kv = 0, qi = 0, tile = 0, tok_ph = 0, fin_ph = 0;
+  uint32_t s_n[2] = {0, 0}, pre_n = 0, o_n = 0;  // phases of the S, o_pre and o_full barriers before this segment
   bool ok = true;
   auto wait = [&](uint64_t *bar, uint32_t par) {
-    bool x = mbar_wait(bar, par, a.timeout_ns, ab);
+    bool x = mbar_sleep(bar, par & 1, a.timeout_ns, ab);
     x = __all_sync(0xffffffffu, x);
     if (!x) ok = false;
     else tc_fence_after_sync();
     return x;
   };
   auto release = [&](uint32_t e) { mbar_arrive(&sc.empty[e % C::NSLOT]); };
+  auto say = [&](uint64_t *bar) {  // the warp's word, behind its writes
+    __syncwarp();
+    if (lane == 0) mbar_arrive(bar);
+  };
   SegmentReader<C> rd;
   while (const Segment *sg = ok ? rd.next_warp(sc, a, ok) : nullptr) {
     const int n = sg->n, ns = sg->ns;
@@ -614,30 +645,38 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
     const uint32_t qe = qi + w;
     qi += 2;
     float m_ref = -CUDART_INF_F, l = 0.f, vref = 0.f;
-    for (int j = 0; j < ns; ++j) {
+    // The other warpgroup's word on step j: take over the reference if it moved. Returns whether it did.
+    auto hear = [&]() {
+      if (!wait(&sc.token[w][wq][p ^ 1], tok_ph)) return false;
+      tok_ph ^= 1;
+      if (*static_cast<volatile int *>(&sc.moved[w][wq][p ^ 1]) == 0) return false;
+      const float m = sc.xm[w][row];
+      if (m_ref != -CUDART_INF_F) l *= ex2_approx(m_ref - m);
+      m_ref = m;
+      return true;
+    };
+    for (int j = NP == 2 ? p : 0; j < ns; j += NP) {
       const int b = j & 1;
-      if (!wait(&sc.s_full[w][b], (s_ph >> b) & 1)) break;
-      s_ph ^= 1u << b;
+      if (!wait(&sc.s_full[w][b], s_n[b] + (j >> 1))) break;
       if constexpr (C::BITS8) {  // the converter's scales (complete: the product above used the same buffers)
         const uint32_t ke = kv + (j & ~1);
-        if (!wait(&sc.full[ke % C::NSLOT], (ke / C::NSLOT) & 1)) break;
+        if (!wait(&sc.full[ke % C::NSLOT], ke / C::NSLOT)) break;
       }
+      const uint32_t s_addr = o_addr + D + b * kStepKeys;
+      uint32_t x[kStepKeys];
+      tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(x));
+      tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
       // The group that produced this S is complete, so this half has done with K of the unit (after its
       // last step), with V of the unit that ended two steps ago, and after the last S with its queries.
       if (leader) {
         if (b == 1 || j == ns - 1) release(kv + (j & ~1));
         if (b == 1 && j >= 3) release(kv + j - 2);
       }
-      // (a complete tile keeps its queries' buffer for its output)
-      if (j == ns - 1 && sg->part >= 0 && lane == 0) mbar_arrive(&sc.q_empty[qe % C::NQ]);
       const int base = sg->u0 * kUnitKeys + j * kStepKeys;
       const int left = lim - base;  // keys of this step that the row sees
-      const bool plain = __all_sync(0xffffffffu, left >= kStepKeys);
-      const uint32_t s_addr = o_addr + D + b * kStepKeys;
       float alpha = 1.f, lsum = 0.f;
       const float *kscale = C::BITS8 ? &sc.ks[(tile + (j >> 1)) % C::NSC][b * kStepKeys] : nullptr;
       const float *vscale = C::BITS8 ? &sc.vs[(tile + (j >> 1)) % C::NSC][b * kStepKeys] : nullptr;
-      uint32_t x[kStepKeys];
       // P = 2^(x f - m) of 32-column chunk c; f: the logit scale, a key's own scale, or 1 (PRE: x is
       // scaled already). POLY: some pairs on the FMA pipe.
       auto exp_chunk = [&](int c, float neg_m, uint64_t(&acc)[2], auto poly_tag, auto pre_tag) {
@@ -680,21 +719,33 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
         f2_split(acc[1], t2, t3);
         return (t0 + t1) + (t2 + t3);
       };
-      tmem_ld32(s_addr, *reinterpret_cast<uint32_t(*)[32]>(x));
-      tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
-      tmem_wait_ld();
-      reg_fence<kStepKeys>(x);
-      bool done = false;
-      if (plain && __all_sync(0xffffffffu, m_ref != -CUDART_INF_F)) {
+      auto exp_fast = [&]() {
         uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 2; ++c) exp_chunk(c, -m_ref, acc, std::true_type{}, std::false_type{});
         lsum = total(acc);
-        done = __all_sync(0xffffffffu, lsum <= kTileSumLimit);
-        if (!done) tmem_wait_st();
+        return __all_sync(0xffffffffu, lsum <= kTileSumLimit);
+      };
+      const bool plain = __all_sync(0xffffffffu, left >= kStepKeys);
+      if (NP == 2 && j == 1) {  // the first reference is the other's
+        hear();
+        if (!ok) break;
+      }
+      bool fast = plain && __all_sync(0xffffffffu, m_ref != -CUDART_INF_F), done = false;
+      tmem_wait_ld();
+      reg_fence<kStepKeys>(x);
+      if (fast) done = exp_fast();
+      if constexpr (NP == 2) {
+        if (j > 1) {
+          const bool moved = hear();
+          if (!ok) break;
+          if (moved) done = false;
+        }
       }
       if (!done) {
-        // With the row maximum: a row's first step, masked steps, and large values.
+        // With the row maximum: a row's first step, masked steps, large values, and a reference that moved.
+        if (fast) tmem_wait_st();
+        fast = false;
 #pragma unroll
         for (int e = 0; e < kStepKeys; ++e) {
           float f = a.scale_log2;
@@ -705,12 +756,23 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
         if (mx > m_ref + kTileSlack) {
           if (m_ref != -CUDART_INF_F) alpha = ex2_approx(m_ref - mx);
           m_ref = mx;
+          fast = true;  // (here: this row's reference moved)
+        }
+        if constexpr (NP == 2) {
+          sc.xm[w][row] = m_ref;
+          fast = __any_sync(0xffffffffu, fast);
         }
         uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 2; ++c)
           exp_chunk(c, m_ref == -CUDART_INF_F ? 0.f : -m_ref, acc, std::false_type{}, std::true_type{});
         lsum = total(acc);
+      } else {
+        fast = false;
+      }
+      if constexpr (NP == 2) {
+        if (lane == 0) sc.moved[w][wq][p] = fast ? 1 : 0;
+        say(&sc.token[w][wq][p]);
       }
       l = l * alpha + lsum;
       if constexpr (C::BITS8) {
@@ -720,8 +782,8 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
         }
       }
       if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
-        // O is at rest once P V of the step before has completed: the other buffer's next commit.
-        if (!wait(&sc.s_full[w][b ^ 1], (s_ph >> (b ^ 1)) & 1)) break;
+        // O is at rest once P V of the step before has completed: its commit is that of S(j + 1), if there is one.
+        if (!(j + 1 < ns ? wait(&sc.s_full[w][b ^ 1], s_n[b ^ 1] + ((j + 1) >> 1)) : wait(&sc.o_pre[w], pre_n))) break;
 #pragma unroll 1
         for (int c = 0; c < D / 32; ++c) {
           uint32_t o[32];
@@ -736,7 +798,7 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
       if (!C::BITS8 && j == ns - 1 && sg->L < base + 16 * step_slices(sg->klim, base)) {
         // The sequence ends inside this step. Both halves write the same zeros, each before its own product.
         const uint32_t ve = kv + (j & ~1) + 1;
-        if (!wait(&sc.full[ve % C::NSLOT], (ve / C::NSLOT) & 1)) break;
+        if (!wait(&sc.full[ve % C::NSLOT], ve / C::NSLOT)) break;
         uint8_t *v = ring + (ve % C::NSLOT) * C::HALF_BYTES + b * (kStepKeys * 128);
         const int r0 = max(sg->L - base, 0), r1 = 16 * step_slices(sg->klim, base);
         for (int e = row; e < (r1 - r0) * 8 * C::PANELS; e += 128) {
@@ -751,26 +813,47 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
     }
     if (!ok) break;
     tile += n;
-    // ---- the last two P V of this half are done: write its rows
-    if (ns > 1) {
-      if (!wait(&sc.s_full[w][ns & 1], (s_ph >> (ns & 1)) & 1)) break;
-      s_ph ^= 1u << (ns & 1);
+    if constexpr (NP == 2) {
+      // The sums of the two warpgroups, both against the last reference: the one without the last step (q)
+      // hears of it and hands its sum over; the other adds and hands the total back.
+      if (p != ((ns - 1) & 1)) {
+        hear();
+        if (!ok) break;
+        sc.xl[w][row] = l;
+        say(&sc.fin[w][wq][p]);
+        if (!wait(&sc.fin[w][wq][p ^ 1], fin_ph)) break;
+        l = sc.xl[w][row];
+      } else {
+        if (!wait(&sc.fin[w][wq][p ^ 1], fin_ph)) break;
+        l += sc.xl[w][row];
+        sc.xl[w][row] = l;
+        say(&sc.fin[w][wq][p]);
+      }
+      fin_ph ^= 1;
     }
-    if (!wait(&sc.s_full[w][(ns - 1) & 1], (s_ph >> ((ns - 1) & 1)) & 1)) break;
-    s_ph ^= 1u << ((ns - 1) & 1);
-    if (leader) {
+    // ---- the last P V of this half (and with it all before) is done: write its rows
+    if (ns > 1 && !wait(&sc.o_pre[w], pre_n)) break;
+    if (!wait(&sc.o_full[w], o_n)) break;
+    pre_n += ns > 1 ? 1 : 0;
+    ++o_n;
+    s_n[0] += (ns + 1) >> 1;
+    s_n[1] += ns >> 1;
+    if (sg->part >= 0 && lane == 0) mbar_arrive(&sc.q_empty[qe % C::NQ]);  // (a complete tile's output goes through it)
+    if (leader && p == 0) {
       // values not returned yet: the steps released those of units before (last odd step - 1) / 2
       const int last = (ns - 1) & 1 ? ns - 1 : ns - 2;  // last odd step, or -1
       for (int i = last >= 3 ? (last - 1) / 2 : 0; i < n; ++i) release(kv + 2 * i + 1);
     }
     kv += 2 * n;
     const float vm = C::BITS8 ? vref : 1.f;
+    // This warpgroup's share of the columns, 32 at a time.
+    constexpr int CH = D / 32 / NP;
     if (sg->part >= 0) {
       // Partial result, [slot][half][column / 4][row][4]: a warp's stores are contiguous.
       const size_t slot = sg->part;
       float *dst = a.part_o + (slot * 2 + w) * (128 * D) + row * 4;
 #pragma unroll 1
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = p * CH; c < (p + 1) * CH; ++c) {
         uint32_t o[32];
         tmem_ld32(o_addr + c * 32, o);
         tmem_wait_ld();
@@ -780,16 +863,20 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
           *reinterpret_cast<float4 *>(dst + (c * 8 + e / 4) * (128 * 4)) =
               make_float4(u2f_(o[e]) * vm, u2f_(o[e + 1]) * vm, u2f_(o[e + 2]) * vm, u2f_(o[e + 3]) * vm);
       }
-      a.part_ml[slot * 512 + w * 128 + row] = m_ref;
-      a.part_ml[slot * 512 + 256 + w * 128 + row] = l;
+      if (p == 0) {
+        a.part_ml[slot * 512 + w * 128 + row] = m_ref;
+        a.part_ml[slot * 512 + 256 + w * 128 + row] = l;
+      }
+      tc_fence_before_sync();
+      mbar_arrive(&sc.o_empty[w]);
     } else {
       // Complete rows: through this half's query buffer (every product with it is done), so that
-      // a warp writes whole rows: its 32 rows one by one would touch 32 lines with every
+      // a warp writes whole lines: its 32 rows one by one would touch 32 lines with every
       // store (measured: 3300 cycles a half, and the stores held up the barriers behind them).
       const float inv = l == 0.f ? 0.f : vm / l;  // a row that sees no key is zero
       uint8_t *buf = q_smem + (qe % C::NQ) * C::HALF_BYTES;
 #pragma unroll
-      for (int c = 0; c < D / 32; ++c) {
+      for (int c = p * CH; c < (p + 1) * CH; ++c) {
         uint32_t o[32];
         tmem_ld32(o_addr + c * 32, o);
         tmem_wait_ld();
@@ -811,24 +898,20 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
           static_cast<long long>(sg->h * a.G + hg) * a.o_head);
       if (!row_ok) dst = 0;
       __syncwarp();
-      constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows of a store
-      const int ch = lane % LPR;
-#pragma unroll 4
+      constexpr int LPR = D / 8 / NP, RPI = 32 / LPR;  // lanes of a row's share, rows of a store
+      const int ch = p * LPR + lane % LPR;
+#pragma unroll 8
       for (int r = 0; r < 32; r += RPI) {
         const int rr = r + lane / LPR;
-        const unsigned long long p = __shfl_sync(0xffffffffu, dst, rr);
+        const unsigned long long ptr = __shfl_sync(0xffffffffu, dst, rr);
         const uint4 v = *reinterpret_cast<const uint4 *>(buf + swz(wq * 32 + rr, ch));
-        if (p) st_global_v4_hint(reinterpret_cast<uint4 *>(p) + ch, v.x, v.y, v.z, v.w, pol_out);
+        if (ptr) st_global_v4_hint(reinterpret_cast<uint4 *>(ptr) + ch, v.x, v.y, v.z, v.w, pol_out);
       }
       // The next copy into the buffer is ordered behind these reads.
       fence_proxy_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sc.q_empty[qe % C::NQ]);
-      rd.done(sc);
-      continue;
     }
-    tc_fence_before_sync();
-    mbar_arrive(&sc.o_empty[w]);
     rd.done(sc);
   }
   if (!ok && lane == 0) tile_abort(&sc.abort_flag, a.status);
@@ -840,8 +923,16 @@ template <class C>
 __global__ void __launch_bounds__(C::THREADS, 1)
     tile_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                 const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ DenseArgs a, const __grid_constant__ TileArgs x) {
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *base = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  extern __shared__ __align__(1024) uint8_t smem_raw[];
+  // The swizzled tiles need 1024-byte alignment, which the start of a block's shared memory has.
+  uint8_t *base = smem_raw;
+  if (smem_u32(smem_raw) & 1023u) {
+    if (threadIdx.x == 0) {
+      atomicCAS(a.status, 0, kStatusTimeoutTile);
+      a.desc[blockIdx.x] = make_int4(0, 0, 0, 0);
+    }
+    return;
+  }
   uint8_t *q_smem = base;
   uint8_t *ring = base + C::NQ * C::HALF_BYTES;
   TileCtl<C> &sc = *reinterpret_cast<TileCtl<C> *>(ring + C::NSLOT * C::HALF_BYTES);
@@ -855,20 +946,26 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     for (int i = 0; i < C::NQ; ++i) {
       mbar_init(&sc.q_full[i], fillers);
-      mbar_init(&sc.q_empty[i], 4);  // the half's softmax warps
+      mbar_init(&sc.q_empty[i], C::SOFTMAX_WARPS / 2);  // the half's softmax warps
     }
     for (int w = 0; w < 2; ++w) {
       for (int b = 0; b < 2; ++b) {
         mbar_init(&sc.s_full[w][b], 1);
         mbar_init(&sc.p_full[w][b], 128);
       }
-      mbar_init(&sc.o_empty[w], 128);
+      mbar_init(&sc.o_pre[w], 1);
+      mbar_init(&sc.o_full[w], 1);
+      mbar_init(&sc.o_empty[w], 128 * C::NP);
+      for (int i = 0; i < 8; ++i) {
+        mbar_init(&sc.token[w][i >> 1][i & 1], 1);
+        mbar_init(&sc.fin[w][i >> 1][i & 1], 1);
+      }
       mbar_init(&sc.mma_done[w], 1);
     }
     mbar_init(&sc.conv, 4);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&sc.seg_full[i], 1);
-      mbar_init(&sc.seg_empty[i], (C::BITS8 ? 128 : 1) + 2 + 256);  // producer or converter, issuers, softmax
+      mbar_init(&sc.seg_empty[i], (C::BITS8 ? 128 : 1) + 2 + 32 * C::SOFTMAX_WARPS);  // producer or converter, issuers, softmax
     }
     sc.turn = 0;
     sc.abort_flag = 0;
@@ -898,7 +995,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   tc_fence_after_sync();
   const uint32_t tmem = sc.tmem_base;
   if (warp < 4) regs_dec<C::CTRL_REGS>();
-  else if (warp < 12) regs_inc<C::SOFTMAX_REGS>();
+  else if (warp < 4 + C::SOFTMAX_WARPS) regs_inc<C::SOFTMAX_REGS>();
   else if constexpr (C::BITS8) regs_inc<C::CONV_REGS>();
   if (warp < 4) {
     if (warp == 0) {
@@ -910,8 +1007,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     } else {
       tile_mma<C>(sc, a, tmem, q_smem, ring, warp == 1 ? 0 : 1);
     }
-  } else if (warp < 12) {
-    tile_softmax<C>(sc, a, tmem, q_smem, ring, (warp - 4) >> 2, warp, lane);
+  } else if (warp < 4 + C::SOFTMAX_WARPS) {
+    tile_softmax<C>(sc, a, tmem, q_smem, ring, (warp - 4) / (4 * C::NP), ((warp - 4) >> 2) % C::NP, warp, lane);
   } else if constexpr (C::BITS8) {
     tile_converter<C>(sc, a, q_smem, ring);
   }

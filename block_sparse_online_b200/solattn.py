@@ -494,22 +494,31 @@ def solattn_selftest_exp2(x: torch.Tensor, stream=None) -> torch.Tensor:
 
 # ---------------------------------------------------------------- dense attention and the cache
 
+_Tensor, _i32, _u8 = torch.Tensor, torch.int32, torch.uint8
+_raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch.cuda.current_device
 
-def _rows(x, name, dtype, shape, device):
-    """Checks a strided tensor of rows of d contiguous elements and returns its strides. The
-    usual case passes on one line: these calls take a few microseconds on the GPU."""
-    if isinstance(x, torch.Tensor) and x.dtype is dtype and x.shape == shape and x.device == device:
-        st = x.stride()
-        if st[-1] == 1 or not x.numel():
-            return st
-        raise ValueError(f"the last dimension of {name} must be contiguous")
+
+def _bad_rows(x, name, dtype, shape, device):
+    """Says what is wrong with a tensor that _rows refused."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if x.dtype is not dtype:
         raise ValueError(f"{name} must have dtype {dtype}, not {x.dtype}")
     if x.shape != shape:
         raise ValueError(f"{name} has shape {tuple(x.shape)}, {tuple(shape)} expected")
-    raise ValueError(f"{name} is on {x.device}, the inputs on {device}")
+    if x.device != device:
+        raise ValueError(f"{name} is on {x.device}, the inputs on {device}")
+    raise ValueError(f"the last dimension of {name} must be contiguous")
+
+
+def _rows(x, name, dtype, shape, device):
+    """Strides of a tensor of rows of d contiguous elements, checked. The usual case passes on one
+    line: these calls take a few microseconds on the GPU."""
+    if isinstance(x, _Tensor) and x.dtype is dtype and x.get_device() == device.index and x.shape == shape:
+        st = x.stride()
+        if st[-1] == 1 or not x.numel():
+            return st
+    _bad_rows(x, name, dtype, shape, device)
 
 
 def _view4(x, name, dtype, shape, device):  # [B, heads, n, d]
@@ -523,7 +532,7 @@ def _view3(x, name, dtype, shape, device):  # packed rows [n, heads, d]
 
 
 def _int32(x, name, numel, device):
-    if not (isinstance(x, torch.Tensor) and x.dtype is torch.int32 and x.device == device and x.is_contiguous()
+    if not (isinstance(x, _Tensor) and x.dtype is _i32 and x.get_device() == device.index and x.is_contiguous()
             and x.numel() >= numel):
         _check_buffer(x, name, (torch.int32,), numel, device)
     return x.data_ptr()
@@ -534,7 +543,7 @@ def _workspace(workspace, need, device):
     if workspace is None:
         workspace = torch.empty(need(), dtype=torch.uint8, device=device)
         workspace[:256].zero_()
-    elif not (isinstance(workspace, torch.Tensor) and workspace.dtype is torch.uint8 and workspace.device == device
+    elif not (isinstance(workspace, _Tensor) and workspace.dtype is _u8 and workspace.get_device() == device.index
               and workspace.is_contiguous()):
         _check_buffer(workspace, "workspace", (torch.uint8, torch.int8), 0, device)
     return workspace
@@ -545,8 +554,8 @@ def _on_device(device, stream, call, *args):
     if stream is not None:
         handle = _stream(stream, device)
     else:
-        handle = torch._C._cuda_getCurrentRawStream(device.index)
-    if torch.cuda.current_device() == device.index:
+        handle = _raw_stream(device.index)
+    if _current_device() == device.index:
         return call(*args, handle)
     with torch.cuda.device(device):
         return call(*args, handle)
