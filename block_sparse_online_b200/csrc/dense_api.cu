@@ -198,8 +198,8 @@ int launch_tiles(DenseArgs a, int dtype, int sms, cudaStream_t st) {
     const cuuint64_t ntok = a.cu ? a.total : a.n;
     const cuuint64_t qd[5] = {D, static_cast<cuuint64_t>(a.G), ntok, static_cast<cuuint64_t>(a.Hkv),
                               static_cast<cuuint64_t>(a.cu ? 1 : a.B)};
-    const long long qs[5] = {1, a.q_head, a.q_tok, a.q_head * a.G, a.q_batch};
     const cuuint32_t qb[5] = {64, static_cast<cuuint32_t>(a.G), static_cast<cuuint32_t>(half), 1, 1};
+    const long long qs[5] = {1, a.q_head, a.q_tok, a.q_head * a.G, a.q_batch};
     const cuuint64_t kd[4] = {D, static_cast<cuuint64_t>(PAGED ? a.page : a.Lmax), static_cast<cuuint64_t>(a.Hkv),
                               static_cast<cuuint64_t>(PAGED ? a.num_pages : a.B)};
     const long long ks[4] = {1, a.k_row, a.k_head, a.k_seq}, vs[4] = {1, a.v_row, a.v_head, a.v_seq};

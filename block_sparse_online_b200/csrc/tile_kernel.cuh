@@ -12,15 +12,10 @@
 //                other half's softmax runs.
 //   warp 2       owns the TMEM allocation; walks the block's range of the line and publishes its
 //                segments (one tile's run of units) to the other roles, a few ahead.
-//   warps 4-19   softmax, two warpgroups for each half (8-bit keys: warps 4-11, one), one row per thread; the
-//                two take the steps in turn. Where a sequence ends inside a step they zero the value rows
-//                behind the end, which may hold anything (0 times NaN is NaN).
+//   warps 4-11   softmax, one warpgroup for each half, one row per thread. Where a sequence ends inside a step they
+//                zero the value rows behind the end, which may hold anything (0 times NaN is NaN).
 //   last 4 warps 8-bit keys only: read codes from the pages, expand them to fp16 into the ring (and the
 //                queries, scaled, into their buffers), one unit ahead in registers.
-// Two warpgroups and one reference: the warpgroup of step j + 1 exponentiates while the one of step j still
-// works, and waits for j's word (a barrier for each 32 rows) that the reference stands before it hands over
-// its P; if it moved, the step is done again. So a step may take two steps' time: with one warpgroup
-// a half the softmax was busy for 1680 of 1845 cycles a step, of which the tensor core needs 1280.
 // A step is 64 keys. Each half has two buffers of S (P takes the place of its S): Q K^T of step j + 2
 // follows P V of step j, so while a warpgroup exponentiates step j + 1 the tensor core works on its steps
 // j and j + 2. With one buffer of 128 keys instead, S, softmax and P V formed one chain of 3700 cycles a
@@ -62,18 +57,15 @@ struct TileCfg {
   static constexpr int NSC = 4;  // units whose scales are kept
   static constexpr int COLS = 128 + D;  // tensor memory columns of a half: O, two buffers of S (and P)
   static constexpr int TMEM_COLS = 512;
-  // Warpgroups of a half's softmax. Two take the steps in turn; the 8-bit kernels have registers for one.
-  static constexpr int NP = 1;
-  static constexpr int SOFTMAX_WARPS = 8 * NP;
-  static constexpr int THREADS = 128 + 32 * SOFTMAX_WARPS + (BITS8 ? 128 : 0);
-  // Register shares: within what the block is launched with (640 x 96, 512 x 128).
+  static constexpr int THREADS = BITS8 ? 512 : 384;
+  // Register shares: within what the block is launched with.
   static constexpr int LAUNCH_REGS = BITS8 ? 128 : 168;
   static constexpr int CTRL_REGS = BITS8 ? 72 : 104;
   static constexpr int CONV_REGS = 136;
   static constexpr int SOFTMAX_REGS = BITS8 ? 152 : 200;
   static_assert(CTRL_REGS < LAUNCH_REGS && (!BITS8 || CONV_REGS > LAUNCH_REGS) && SOFTMAX_REGS > LAUNCH_REGS,
                 "control warps give registers up, the others take them");
-  static_assert(128 * CTRL_REGS + 32 * SOFTMAX_WARPS * SOFTMAX_REGS + (BITS8 ? 128 * CONV_REGS : 0) <= THREADS * LAUNCH_REGS,
+  static_assert(128 * CTRL_REGS + 256 * SOFTMAX_REGS + (BITS8 ? 128 * CONV_REGS : 0) <= THREADS * LAUNCH_REGS,
                 "register split");
   static constexpr bool FP16 = std::is_same<MT, __half>::value;
   static constexpr uint32_t IDESC_PV = idesc_16bit_f32(128, D, true, FP16);
@@ -99,15 +91,11 @@ struct TileCtl {
   uint64_t q_full[C::NQ], q_empty[C::NQ];
   uint64_t s_full[2][2], p_full[2][2];  // by half, and buffer of S
   uint64_t o_pre[2], o_full[2], o_empty[2];  // the tile's last product but one, its last, and O read
-  uint64_t token[2][4][2];  // [half][32 rows][warpgroup]: the reference of its step stands
-  uint64_t fin[2][4][2];    // the same rows at the end of a tile
   uint64_t conv;  // the converter's four warps
   uint64_t mma_done[2];
   uint32_t turn;
   uint32_t tmem_base;
   int abort_flag;
-  int moved[2][4][2];            // a reference of these rows moved in the warpgroup's last step
-  float xm[C::NP == 2 ? 2 : 1][128], xl[C::NP == 2 ? 2 : 1][128];  // references and sums between the warpgroups of a half
   float wmax[2][4];              // converter: largest value scale per warp
   alignas(16) float ks[C::BITS8 ? C::NSC : 1][C::BITS8 ? 128 : 4];  // key scales (x log2(e) / sqrt d)
   alignas(16) float vs[C::BITS8 ? C::NSC : 1][C::BITS8 ? 128 : 4];  // value scales over the reference
@@ -606,11 +594,11 @@ __device__ void tile_mma(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint
 
 // ------------------------------------------------------------------ softmax and epilogue
 
-// w: half of the tile; p: which of its warpgroups (NP = 2: steps p, p + 2, ..., all in S buffer p).
+// w: half of the tile.
 template <class C>
-__device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint8_t *q_smem, uint8_t *ring, int w, int p,
-                             int warp, int lane) {
-  constexpr int D = C::D, NP = C::NP;
+__device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint8_t *q_smem, uint8_t *ring,
+                             int w, int warp, int lane) {
+  constexpr int D = C::D;
   using QT = typename C::QT;
   using MT = typename C::MT;
   const volatile int *ab = &sc.abort_flag;
@@ -618,7 +606,7 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
   const uint32_t o_addr = tmem + (static_cast<uint32_t>(wq * 32) << 16) + w * C::COLS;
   const bool leader = row == 0;  // of its warpgroup
   const uint64_t pol_out = l2_policy_evict_first();
-  uint32_t kv = 0, qi = 0, tile = 0, tok_ph = 0, fin_ph = 0;
+  uint32_t kv = 0, qi = 0, tile = 0;
   uint32_t s_n[2] = {0, 0}, pre_n = 0, o_n = 0;  // phases of the S, o_pre and o_full barriers before this segment
   bool ok = true;
   auto wait = [&](uint64_t *bar, uint32_t par) {
@@ -629,33 +617,17 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
     return x;
   };
   auto release = [&](uint32_t e) { mbar_arrive(&sc.empty[e % C::NSLOT]); };
-  auto say = [&](uint64_t *bar) {  // the warp's word, behind its writes
-    __syncwarp();
-    if (lane == 0) mbar_arrive(bar);
-  };
+  // The row's token (from the tile's first) and head of the group.
+  const int half = a.tile_tokens >> 1, my_i = row / a.G, my_hg = row - my_i * a.G, my_tok = w * half + my_i;
+  auto row_in = [&](const Segment &g) { return my_i < half && g.tok + my_tok < g.end; };
   SegmentReader<C> rd;
   while (const Segment *sg = ok ? rd.next_warp(sc, a, ok) : nullptr) {
     const int n = sg->n, ns = sg->ns;
-    int lim;
-    {
-      int tok, hg;
-      const bool row_ok = half_row(a, *sg, w, row, tok, hg);
-      lim = row_ok ? (a.causal ? min(max(sg->lim0 + tok, 0), sg->L) : sg->L) : sg->klim;
-    }
+    const int lim = row_in(*sg) ? (a.causal ? min(max(sg->lim0 + my_tok, 0), sg->L) : sg->L) : sg->klim;
     const uint32_t qe = qi + w;
     qi += 2;
     float m_ref = -CUDART_INF_F, l = 0.f, vref = 0.f;
-    // The other warpgroup's word on step j: take over the reference if it moved. Returns whether it did.
-    auto hear = [&]() {
-      if (!wait(&sc.token[w][wq][p ^ 1], tok_ph)) return false;
-      tok_ph ^= 1;
-      if (*static_cast<volatile int *>(&sc.moved[w][wq][p ^ 1]) == 0) return false;
-      const float m = sc.xm[w][row];
-      if (m_ref != -CUDART_INF_F) l *= ex2_approx(m_ref - m);
-      m_ref = m;
-      return true;
-    };
-    for (int j = NP == 2 ? p : 0; j < ns; j += NP) {
+    for (int j = 0; j < ns; ++j) {
       const int b = j & 1;
       if (!wait(&sc.s_full[w][b], s_n[b] + (j >> 1))) break;
       if constexpr (C::BITS8) {  // the converter's scales (complete: the product above used the same buffers)
@@ -678,9 +650,9 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
       const float *kscale = C::BITS8 ? &sc.ks[(tile + (j >> 1)) % C::NSC][b * kStepKeys] : nullptr;
       const float *vscale = C::BITS8 ? &sc.vs[(tile + (j >> 1)) % C::NSC][b * kStepKeys] : nullptr;
       // P = 2^(x f - m) of 32-column chunk c; f: the logit scale, a key's own scale, or 1 (PRE: x is
-      // scaled already). POLY: some pairs on the FMA pipe.
-      auto exp_chunk = [&](int c, float neg_m, uint64_t(&acc)[2], auto poly_tag, auto pre_tag) {
-        constexpr bool POLY = decltype(poly_tag)::value, PRE = decltype(pre_tag)::value;
+      // scaled already).
+      auto exp_chunk = [&](int c, float neg_m, uint64_t(&acc)[2], auto pre_tag) {
+        constexpr bool PRE = decltype(pre_tag)::value;
         const uint64_t nmp = f2(neg_m, neg_m);
         uint32_t pk[16];
 #pragma unroll
@@ -697,7 +669,7 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
             else xx = fma2(v, f2(a.scale_log2, a.scale_log2), nmp);
             float x0, x1, p0, p1;
             f2_split(xx, x0, x1);
-            if (POLY && ((kTilePolyMask >> ((e + t) % 8)) & 1u)) {
+            if (((kTilePolyMask >> ((e + t) % 8)) & 1u) != 0u) {
               exp2_poly_nan_x2(x0, x1, p0, p1);
             } else {
               p0 = ex2_approx(x0);
@@ -722,57 +694,39 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
       auto exp_fast = [&]() {
         uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
-        for (int c = 0; c < 2; ++c) exp_chunk(c, -m_ref, acc, std::true_type{}, std::false_type{});
+        for (int c = 0; c < 2; ++c) exp_chunk(c, -m_ref, acc, std::false_type{});
         lsum = total(acc);
         return __all_sync(0xffffffffu, lsum <= kTileSumLimit);
       };
       const bool plain = __all_sync(0xffffffffu, left >= kStepKeys);
-      if (NP == 2 && j == 1) {  // the first reference is the other's
-        hear();
-        if (!ok) break;
-      }
-      bool fast = plain && __all_sync(0xffffffffu, m_ref != -CUDART_INF_F), done = false;
+      bool done = false;
       tmem_wait_ld();
       reg_fence<kStepKeys>(x);
-      if (fast) done = exp_fast();
-      if constexpr (NP == 2) {
-        if (j > 1) {
-          const bool moved = hear();
-          if (!ok) break;
-          if (moved) done = false;
-        }
+      if (plain && __all_sync(0xffffffffu, m_ref != -CUDART_INF_F)) {
+        done = exp_fast();
+        if (!done) tmem_wait_st();
       }
       if (!done) {
-        // With the row maximum: a row's first step, masked steps, large values, and a reference that moved.
-        if (fast) tmem_wait_st();
-        fast = false;
+        // With the row maximum (a NaN wins and takes the row): a row's first step, masked steps, and large values.
 #pragma unroll
         for (int e = 0; e < kStepKeys; ++e) {
           float f = a.scale_log2;
           if constexpr (C::BITS8) f = kscale[e];
           x[e] = e < left ? __float_as_uint(u2f_(x[e]) * f) : __float_as_uint(-CUDART_INF_F);
         }
-        const float mx = max_tree_bits<kStepKeys>(x);
-        if (mx > m_ref + kTileSlack) {
+        float mxs[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
+#pragma unroll
+        for (int e = 0; e < kStepKeys; e += 2) mxs[(e >> 1) & 3] = fmax3_nan(mxs[(e >> 1) & 3], u2f_(x[e]), u2f_(x[e + 1]));
+        const float mx = fmax3_nan(mxs[0], mxs[1], fmax3_nan(mxs[2], mxs[3], mxs[3]));
+        if (!(mx <= m_ref + kTileSlack)) {
           if (m_ref != -CUDART_INF_F) alpha = ex2_approx(m_ref - mx);
           m_ref = mx;
-          fast = true;  // (here: this row's reference moved)
-        }
-        if constexpr (NP == 2) {
-          sc.xm[w][row] = m_ref;
-          fast = __any_sync(0xffffffffu, fast);
         }
         uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          exp_chunk(c, m_ref == -CUDART_INF_F ? 0.f : -m_ref, acc, std::false_type{}, std::true_type{});
+          exp_chunk(c, m_ref == -CUDART_INF_F ? 0.f : -m_ref, acc, std::true_type{});
         lsum = total(acc);
-      } else {
-        fast = false;
-      }
-      if constexpr (NP == 2) {
-        if (lane == 0) sc.moved[w][wq][p] = fast ? 1 : 0;
-        say(&sc.token[w][wq][p]);
       }
       l = l * alpha + lsum;
       if constexpr (C::BITS8) {
@@ -813,24 +767,6 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
     }
     if (!ok) break;
     tile += n;
-    if constexpr (NP == 2) {
-      // The sums of the two warpgroups, both against the last reference: the one without the last step (q)
-      // hears of it and hands its sum over; the other adds and hands the total back.
-      if (p != ((ns - 1) & 1)) {
-        hear();
-        if (!ok) break;
-        sc.xl[w][row] = l;
-        say(&sc.fin[w][wq][p]);
-        if (!wait(&sc.fin[w][wq][p ^ 1], fin_ph)) break;
-        l = sc.xl[w][row];
-      } else {
-        if (!wait(&sc.fin[w][wq][p ^ 1], fin_ph)) break;
-        l += sc.xl[w][row];
-        sc.xl[w][row] = l;
-        say(&sc.fin[w][wq][p]);
-      }
-      fin_ph ^= 1;
-    }
     // ---- the last P V of this half (and with it all before) is done: write its rows
     if (ns > 1 && !wait(&sc.o_pre[w], pre_n)) break;
     if (!wait(&sc.o_full[w], o_n)) break;
@@ -839,21 +775,19 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
     s_n[0] += (ns + 1) >> 1;
     s_n[1] += ns >> 1;
     if (sg->part >= 0 && lane == 0) mbar_arrive(&sc.q_empty[qe % C::NQ]);  // (a complete tile's output goes through it)
-    if (leader && p == 0) {
+    if (leader) {
       // values not returned yet: the steps released those of units before (last odd step - 1) / 2
       const int last = (ns - 1) & 1 ? ns - 1 : ns - 2;  // last odd step, or -1
       for (int i = last >= 3 ? (last - 1) / 2 : 0; i < n; ++i) release(kv + 2 * i + 1);
     }
     kv += 2 * n;
     const float vm = C::BITS8 ? vref : 1.f;
-    // This warpgroup's share of the columns, 32 at a time.
-    constexpr int CH = D / 32 / NP;
     if (sg->part >= 0) {
       // Partial result, [slot][half][column / 4][row][4]: a warp's stores are contiguous.
       const size_t slot = sg->part;
       float *dst = a.part_o + (slot * 2 + w) * (128 * D) + row * 4;
 #pragma unroll 1
-      for (int c = p * CH; c < (p + 1) * CH; ++c) {
+      for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         tmem_ld32(o_addr + c * 32, o);
         tmem_wait_ld();
@@ -863,10 +797,8 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
           *reinterpret_cast<float4 *>(dst + (c * 8 + e / 4) * (128 * 4)) =
               make_float4(u2f_(o[e]) * vm, u2f_(o[e + 1]) * vm, u2f_(o[e + 2]) * vm, u2f_(o[e + 3]) * vm);
       }
-      if (p == 0) {
-        a.part_ml[slot * 512 + w * 128 + row] = m_ref;
-        a.part_ml[slot * 512 + 256 + w * 128 + row] = l;
-      }
+      a.part_ml[slot * 512 + w * 128 + row] = m_ref;
+      a.part_ml[slot * 512 + 256 + w * 128 + row] = l;
       tc_fence_before_sync();
       mbar_arrive(&sc.o_empty[w]);
     } else {
@@ -876,7 +808,7 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
       const float inv = l == 0.f ? 0.f : vm / l;  // a row that sees no key is zero
       uint8_t *buf = q_smem + (qe % C::NQ) * C::HALF_BYTES;
 #pragma unroll
-      for (int c = p * CH; c < (p + 1) * CH; ++c) {
+      for (int c = 0; c < D / 32; ++c) {
         uint32_t o[32];
         tmem_ld32(o_addr + c * 32, o);
         tmem_wait_ld();
@@ -891,15 +823,13 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
       }
       tc_fence_before_sync();
       mbar_arrive(&sc.o_empty[w]);
-      int tok, hg;
-      const bool row_ok = half_row(a, *sg, w, row, tok, hg);
       unsigned long long dst = reinterpret_cast<unsigned long long>(
-          static_cast<QT *>(a.out) + sg->b * a.o_batch + static_cast<long long>(sg->tok + tok) * a.o_tok +
-          static_cast<long long>(sg->h * a.G + hg) * a.o_head);
-      if (!row_ok) dst = 0;
+          static_cast<QT *>(a.out) + sg->b * a.o_batch + static_cast<long long>(sg->tok + my_tok) * a.o_tok +
+          static_cast<long long>(sg->h * a.G + my_hg) * a.o_head);
+      if (!row_in(*sg)) dst = 0;
       __syncwarp();
-      constexpr int LPR = D / 8 / NP, RPI = 32 / LPR;  // lanes of a row's share, rows of a store
-      const int ch = p * LPR + lane % LPR;
+      constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows of a store
+      const int ch = lane % LPR;
 #pragma unroll 8
       for (int r = 0; r < 32; r += RPI) {
         const int rr = r + lane / LPR;
@@ -946,7 +876,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
     for (int i = 0; i < C::NQ; ++i) {
       mbar_init(&sc.q_full[i], fillers);
-      mbar_init(&sc.q_empty[i], C::SOFTMAX_WARPS / 2);  // the half's softmax warps
+      mbar_init(&sc.q_empty[i], 4);  // the half's softmax warps
     }
     for (int w = 0; w < 2; ++w) {
       for (int b = 0; b < 2; ++b) {
@@ -955,17 +885,13 @@ __global__ void __launch_bounds__(C::THREADS, 1)
       }
       mbar_init(&sc.o_pre[w], 1);
       mbar_init(&sc.o_full[w], 1);
-      mbar_init(&sc.o_empty[w], 128 * C::NP);
-      for (int i = 0; i < 8; ++i) {
-        mbar_init(&sc.token[w][i >> 1][i & 1], 1);
-        mbar_init(&sc.fin[w][i >> 1][i & 1], 1);
-      }
+      mbar_init(&sc.o_empty[w], 128);
       mbar_init(&sc.mma_done[w], 1);
     }
     mbar_init(&sc.conv, 4);
     for (int i = 0; i < kSegs; ++i) {
       mbar_init(&sc.seg_full[i], 1);
-      mbar_init(&sc.seg_empty[i], (C::BITS8 ? 128 : 1) + 2 + 32 * C::SOFTMAX_WARPS);  // producer or converter, issuers, softmax
+      mbar_init(&sc.seg_empty[i], (C::BITS8 ? 128 : 1) + 2 + 256);  // producer or converter, issuers, softmax
     }
     sc.turn = 0;
     sc.abort_flag = 0;
@@ -995,7 +921,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   tc_fence_after_sync();
   const uint32_t tmem = sc.tmem_base;
   if (warp < 4) regs_dec<C::CTRL_REGS>();
-  else if (warp < 4 + C::SOFTMAX_WARPS) regs_inc<C::SOFTMAX_REGS>();
+  else if (warp < 12) regs_inc<C::SOFTMAX_REGS>();
   else if constexpr (C::BITS8) regs_inc<C::CONV_REGS>();
   if (warp < 4) {
     if (warp == 0) {
@@ -1007,8 +933,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     } else {
       tile_mma<C>(sc, a, tmem, q_smem, ring, warp == 1 ? 0 : 1);
     }
-  } else if (warp < 4 + C::SOFTMAX_WARPS) {
-    tile_softmax<C>(sc, a, tmem, q_smem, ring, (warp - 4) / (4 * C::NP), ((warp - 4) >> 2) % C::NP, warp, lane);
+  } else if (warp < 12) {
+    tile_softmax<C>(sc, a, tmem, q_smem, ring, (warp - 4) >> 2, warp, lane);
   } else if constexpr (C::BITS8) {
     tile_converter<C>(sc, a, q_smem, ring);
   }
