@@ -7,8 +7,9 @@
 // head of the group) pairs, token-major, so shared key heads fill a tile's rows and every
 // key is read once for all of them. The rows are cut into tiles; the keys into units of 128.
 //
-// Schedule. The units of all (sequence, key head, row tile) items, in that order, form one
-// line of W units, which the P blocks of the launch share evenly: block c takes units
+// Schedule. The units of all (sequence, key head, row tile) items, in that order, each item's behind a few
+// places that stand for its fixed cost (queries in, rows out), form one
+// line of W places, which the P blocks of the launch share evenly: block c takes places
 // [c W / P, (c + 1) W / P). Lengths live on the device, so the line is laid out there: each
 // warp scans the sequences' work once at its start (B values, 32 at a time). A block whose
 // range begins or ends inside an item leaves an unnormalised partial result (row maximum,
@@ -87,6 +88,7 @@ __device__ __forceinline__ int key_limit(const DenseArgs &a, const Seq &s, int t
 template <int RT_>
 struct RowTiles {
   static constexpr int RT = RT_;
+  static constexpr int COST = 1;  // an item's fixed cost in units
   static __device__ __forceinline__ int tiles(const DenseArgs &a, int n) { return (n * a.G + RT - 1) / RT; }
   static __device__ __forceinline__ int last_token(const DenseArgs &a, int n, int t) {
     return (min(n * a.G, (t + 1) * RT) - 1) / a.G;
@@ -103,6 +105,9 @@ struct RowTiles {
 // the last whole token of a half are empty), as a box copy of (heads of the group, tokens) lays them.
 struct TokenTiles {
   static constexpr int RT = 256;
+  // A tile costs about 5500 cycles and 3700 a unit. (Without it blocks of many short items finish last: a
+  // batch of prompts of 0 to 256 keys lost 15 % to that.)
+  static constexpr int COST = 2;
   static __device__ __forceinline__ int tiles(const DenseArgs &a, int n) {
     return (n + a.tile_tokens - 1) / a.tile_tokens;
   }
@@ -123,13 +128,13 @@ __device__ __forceinline__ int item_units(const DenseArgs &a, const Seq &s, int 
   return max(1, (key_limit(a, s, T::last_token(a, s.n, t)) + kUnitKeys - 1) / kUnitKeys);
 }
 
-// Units of one key head of sequence b.
+// Places of one key head of sequence b.
 template <class T>
-__device__ __forceinline__ long long head_units(const DenseArgs &a, const Seq &s) {
+__device__ __forceinline__ long long head_places(const DenseArgs &a, const Seq &s) {
   const int tiles = T::tiles(a, s.n);
-  if (!a.causal) return static_cast<long long>(tiles) * max(1, (s.L + kUnitKeys - 1) / kUnitKeys);
+  if (!a.causal) return static_cast<long long>(tiles) * (T::COST + max(1, (s.L + kUnitKeys - 1) / kUnitKeys));
   long long w = 0;
-  for (int t = 0; t < tiles; ++t) w += item_units<T>(a, s, t);
+  for (int t = 0; t < tiles; ++t) w += T::COST + item_units<T>(a, s, t);
   return w;
 }
 
@@ -137,11 +142,11 @@ __device__ __forceinline__ long long head_units(const DenseArgs &a, const Seq &s
 // it the cursor is the same in every lane and step() needs no other lane.
 template <class T>
 struct Cursor {
-  long long x, x1, W;  // next unit, end of the range, length of the line
+  long long x, x1, W;  // next place, end of the range, length of the line
   int P;               // blocks that share the line
   bool whole;
   Seq s;
-  int b, h, t, tiles, units, u0, u1;
+  int b, h, t, tiles, units, o0, o1, u0, u1;  // o0, o1: the segment's places in its item; u0, u1: its units
 
   __device__ __forceinline__ long long bound(int c) const { return W * c / P; }
 
@@ -154,7 +159,7 @@ struct Cursor {
       long long w = 0, it = 0;
       if (b0 + lane < a.B) {
         const Seq q = seq_of(a, b0 + lane);
-        w = head_units<T>(a, q) * a.Hkv;
+        w = head_places<T>(a, q) * a.Hkv;
         it = static_cast<long long>(T::tiles(a, q.n)) * a.Hkv;
       }
 #pragma unroll
@@ -177,7 +182,7 @@ struct Cursor {
     int found = -1;
     for (int b0 = 0; b0 < a.B && found < 0; b0 += 32) {
       long long w = 0;
-      if (b0 + lane < a.B) w = head_units<T>(a, seq_of(a, b0 + lane)) * a.Hkv;
+      if (b0 + lane < a.B) w = head_places<T>(a, seq_of(a, b0 + lane)) * a.Hkv;
       long long incl = w;
 #pragma unroll
       for (int o = 1; o < 32; o <<= 1) {
@@ -196,37 +201,41 @@ struct Cursor {
     b = found;
     s = seq_of(a, b);
     tiles = T::tiles(a, s.n);
-    const long long per_head = head_units<T>(a, s);
+    const long long per_head = head_places<T>(a, s);
     h = static_cast<int>(rem / per_head);
     rem -= per_head * h;
     t = 0;
     if (!a.causal) {
       units = item_units<T>(a, s, 0);
-      t = static_cast<int>(rem / units);
-      rem -= static_cast<long long>(units) * t;
+      t = static_cast<int>(rem / (T::COST + units));
+      rem -= static_cast<long long>(T::COST + units) * t;
     } else {
       for (;; ++t) {
         units = item_units<T>(a, s, t);
-        if (rem < units) break;
-        rem -= units;
+        if (rem < T::COST + units) break;
+        rem -= T::COST + units;
       }
     }
-    u0 = static_cast<int>(rem);
-    if (whole && u0 > 0) {  // the item begins in an earlier block's range
-      x += units - u0;
+    o0 = static_cast<int>(rem);
+    if (whole && o0 > 0) {  // the item begins in an earlier block's range
+      x += T::COST + units - o0;
       next_item(a);
-      if (x >= x1) return false;
+      if (x >= x1 || b >= a.B) return false;
     }
-    set_end();
-    return true;
+    return set_end();
   }
 
-  __device__ __forceinline__ void set_end() {
-    u1 = whole ? units : static_cast<int>(min(static_cast<long long>(units), u0 + (x1 - x)));
+  // False where the range ends before the item's first unit: the next block then takes the item.
+  __device__ __forceinline__ bool set_end() {
+    const int span = T::COST + units;
+    o1 = whole ? span : static_cast<int>(min(static_cast<long long>(span), o0 + (x1 - x)));
+    u0 = max(0, o0 - T::COST);
+    u1 = max(0, o1 - T::COST);
+    return u1 > 0;
   }
 
   __device__ __forceinline__ void next_item(const DenseArgs &a) {
-    u0 = 0;
+    o0 = 0;
     if (++t == tiles) {
       t = 0;
       if (++h == a.Hkv) {
@@ -244,12 +253,11 @@ struct Cursor {
 
   // The next segment of the range; false at its end.
   __device__ __forceinline__ bool step(const DenseArgs &a) {
-    x += u1 - u0;
+    x += o1 - o0;
     if (x >= x1) return false;
     next_item(a);
     if (b >= a.B) return false;
-    set_end();
-    return true;
+    return set_end();
   }
 
   __device__ __forceinline__ bool partial() const { return u0 > 0 || u1 < units; }
@@ -257,7 +265,7 @@ struct Cursor {
   // The record of an item that this block begins and other blocks end.
   __device__ __forceinline__ int4 record(int c) const {
     int e = c;
-    while (bound(e + 1) < x + units) ++e;
+    while (bound(e + 1) < x - o0 + T::COST + units) ++e;
     return make_int4(e - c + 1, b, h, t);
   }
 };

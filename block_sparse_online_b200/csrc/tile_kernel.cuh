@@ -184,17 +184,8 @@ __device__ void tile_scheduler(TileCtl<C> &sc, const DenseArgs &a, const TileArg
 template <class C>
 struct SegmentReader {
   uint32_t i = 0;
-  // The next segment, or null at the end (or when a wait gave up: ok is cleared).
+  // The next segment, or null at the end (or when a wait gave up: ok is cleared). The whole warp calls it.
   __device__ __forceinline__ const Segment *next(TileCtl<C> &sc, const DenseArgs &a, bool &ok) {
-    const int sl = i % kSegs;
-    if (!mbar_sleep(&sc.seg_full[sl], (i / kSegs) & 1, a.timeout_ns, &sc.abort_flag)) {
-      ok = false;
-      return nullptr;
-    }
-    ++i;
-    return sc.seg[sl].n ? &sc.seg[sl] : nullptr;
-  }
-  __device__ __forceinline__ const Segment *next_warp(TileCtl<C> &sc, const DenseArgs &a, bool &ok) {
     const int sl = i % kSegs;
     if (!__all_sync(0xffffffffu, mbar_sleep(&sc.seg_full[sl], (i / kSegs) & 1, a.timeout_ns, &sc.abort_flag))) {
       ok = false;
@@ -217,63 +208,77 @@ __device__ __forceinline__ bool half_row(const DenseArgs &a, const Segment &g, i
 
 // ------------------------------------------------------------------ TMA producer (16-bit keys)
 
+// The whole warp walks along: lane 0 keeps the barriers, and the copies of a buffer (one a panel, or a
+// panel and page) are issued by as many lanes at once. Pages are looked up a unit ahead, one by each of those lanes: with
+// pages of 16 tokens a single thread's 16 lookups and 32 copies took longer than the unit's products.
 template <class C>
-__device__ void tile_producer(TileCtl<C> &sc, const DenseArgs &a, const TileArgs &x, uint8_t *q_smem, uint8_t *ring, const CUtensorMap *tm_q, const CUtensorMap *tm_k, const CUtensorMap *tm_v) {
+__device__ void tile_producer(TileCtl<C> &sc, const DenseArgs &a, const TileArgs &x, uint8_t *q_smem, uint8_t *ring,
+                              const CUtensorMap *tm_q, const CUtensorMap *tm_k, const CUtensorMap *tm_v, int lane) {
   const volatile int *ab = &sc.abort_flag;
   const uint64_t pol_stream = l2_policy_evict_first(), pol_reuse = l2_policy_evict_last();
   const int half = a.tile_tokens >> 1;
   const uint32_t q_bytes = static_cast<uint32_t>(half) * a.G * 128;  // of a panel
+  const int boxes = C::PAGED ? kUnitKeys >> a.page_shift : 1;        // of a panel of a unit
+  const int box = lane % boxes, pn = lane / boxes;                   // this lane's copy of a unit's K or V
+  const bool mine = pn < C::PANELS;
   uint32_t kv = 0, qi = 0;
   bool ok = true;
+  auto wait = [&](uint64_t *bar, uint32_t par) { return __all_sync(0xffffffffu, mbar_sleep(bar, par, a.timeout_ns, ab)); };
   SegmentReader<C> rd;
   while (const Segment *g = ok ? rd.next(sc, a, ok) : nullptr) {
     const int b = g->b, h = g->h, L = g->L, tok0 = g->tok, u0 = g->u0, u1 = u0 + g->n;
-    rd.done(sc);
+    __syncwarp();
+    if (lane == 0) rd.done(sc);
     auto load_q = [&](int w) {
       const int sl = qi % C::NQ;
-      if (!mbar_sleep(&sc.q_empty[sl], ((qi / C::NQ) & 1) ^ 1, a.timeout_ns, ab)) return false;
-      mbar_arrive_expect_tx(&sc.q_full[sl], q_bytes * C::PANELS);
-      const int tok = tok0 + w * half;
-#pragma unroll
-      for (int pn = 0; pn < C::PANELS; ++pn)
-        tma_load_5d_hint(smem_u32(q_smem + sl * C::HALF_BYTES + pn * (128 * 128)), tm_q, smem_u32(&sc.q_full[sl]), pn * 64, 0,
-                         tok, h, a.cu ? 0 : b, pol_stream);
+      if (!wait(&sc.q_empty[sl], ((qi / C::NQ) & 1) ^ 1)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&sc.q_full[sl], q_bytes * C::PANELS);
+      __syncwarp();
+      if (lane < C::PANELS)
+        tma_load_5d_hint(smem_u32(q_smem + sl * C::HALF_BYTES + lane * (128 * 128)), tm_q, smem_u32(&sc.q_full[sl]), lane * 64, 0,
+                         tok0 + w * half, h, a.cu ? 0 : b, pol_stream);
       ++qi;
       return true;
     };
-    auto load_kv = [&](int u, bool is_v) {
+    // Page of this lane's box of unit u. Keys behind the end, and bad table entries, lie outside the map: they
+    // read as zeros.
+    auto page_at = [&](int u) {
+      const int j = u * kUnitKeys + (box << a.page_shift);
+      int id = -1;
+      if (mine && u < u1 && j < L) id = page_of(a, b, j);
+      return id < 0 ? a.num_pages : id;
+    };
+    auto load_kv = [&](int u, bool is_v, int page) {
       const int sl = kv % C::NSLOT;
-      if (!mbar_sleep(&sc.empty[sl], ((kv / C::NSLOT) & 1) ^ 1, a.timeout_ns, ab)) return false;
-      mbar_arrive_expect_tx(&sc.full[sl], C::HALF_BYTES);
-      const CUtensorMap *map = is_v ? tm_v : tm_k;
-      uint8_t *dst = ring + sl * C::HALF_BYTES;
-      if constexpr (C::PAGED) {
-        for (int r = 0; r < kUnitKeys; r += a.page) {
-          const int j = u * kUnitKeys + r;
-          // keys behind the end, and bad table entries, lie outside the map: they read as zeros
-          int id = -1;
-          if (j < L) id = page_of(a, b, j);
-          if (id < 0) id = a.num_pages;
-#pragma unroll
-          for (int pn = 0; pn < C::PANELS; ++pn)
-            tma_load_4d_hint(smem_u32(dst + pn * (128 * 128) + r * 128), map, smem_u32(&sc.full[sl]), pn * 64, 0, h, id, pol_reuse);
-        }
-      } else {
-#pragma unroll
-        for (int pn = 0; pn < C::PANELS; ++pn)
-          tma_load_4d_hint(smem_u32(dst + pn * (128 * 128)), map, smem_u32(&sc.full[sl]), pn * 64, u * kUnitKeys,
-                           h * (is_v ? x.v_h : x.k_h), b * (is_v ? x.v_b : x.k_b), pol_reuse);
+      if (!wait(&sc.empty[sl], ((kv / C::NSLOT) & 1) ^ 1)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&sc.full[sl], C::HALF_BYTES);
+      __syncwarp();
+      if (mine) {
+        const CUtensorMap *map = is_v ? tm_v : tm_k;
+        uint8_t *dst = ring + sl * C::HALF_BYTES + pn * (128 * 128);
+        if constexpr (C::PAGED)
+          tma_load_4d_hint(smem_u32(dst + (box << a.page_shift) * 128), map, smem_u32(&sc.full[sl]), pn * 64, 0, h, page, pol_reuse);
+        else
+          tma_load_4d_hint(smem_u32(dst), map, smem_u32(&sc.full[sl]), pn * 64, u * kUnitKeys, h * (is_v ? x.v_h : x.k_h),
+                           b * (is_v ? x.v_b : x.k_b), pol_reuse);
       }
       ++kv;
       return true;
     };
-    ok = load_q(0) && load_kv(u0, false) && load_q(1);
+    int page = 0, next = 0;
+    if constexpr (C::PAGED) {
+      page = page_at(u0);
+      next = page_at(u0 + 1);
+    }
+    ok = load_q(0) && load_kv(u0, false, page) && load_q(1);
     for (int u = u0; u < u1 && ok; ++u) {
-      ok = load_kv(u, true);
-      if (ok && u + 1 < u1) ok = load_kv(u + 1, false);
+      ok = load_kv(u, true, page);
+      page = next;
+      if (ok && u + 1 < u1) ok = load_kv(u + 1, false, page);
+      if constexpr (C::PAGED) next = page_at(u + 2);
     }
   }
-  if (!ok) tile_abort(&sc.abort_flag, a.status);
+  if (!ok && lane == 0) tile_abort(&sc.abort_flag, a.status);
   // No copy may outlive the block: wait (bounded) for the last fill of every buffer.
   const int zero = 0;
   for (uint32_t f = kv > C::NSLOT ? kv - C::NSLOT : 0; f < kv; ++f)
@@ -359,7 +364,7 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
     mbar_arrive(bar);  // 128 arrivals
   };
   SegmentReader<C> rd;
-  const Segment *g = rd.next_warp(sc, a, ok);
+  const Segment *g = rd.next(sc, a, ok);
   if (g) {
     const int pages = fetch_pages(*g, g->u0);
     fetch(*g, g->u0, pages, false, ck);
@@ -439,7 +444,7 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
       int fu = u + 1;
       if (fu == u1) {
         rd.done(sc);
-        f = nxt = rd.next_warp(sc, a, ok);
+        f = nxt = rd.next(sc, a, ok);
         if (f) fu = f->u0;
       }
       const int pages = f ? fetch_pages(*f, fu) : -1;
@@ -528,7 +533,7 @@ __device__ void tile_mma(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, uint
     __syncwarp();
   };
   SegmentReader<C> rd;
-  while (const Segment *sg = ok ? rd.next_warp(sc, a, ok) : nullptr) {
+  while (const Segment *sg = ok ? rd.next(sc, a, ok) : nullptr) {
     // (a broadcast tells the compiler that the values are the same in every lane)
     const int n = __shfl_sync(0xffffffffu, sg->n, 0), ns = __shfl_sync(0xffffffffu, sg->ns, 0);
     const int klim = __shfl_sync(0xffffffffu, sg->klim, 0), base = __shfl_sync(0xffffffffu, sg->u0, 0) * kUnitKeys;
@@ -621,7 +626,7 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
   const int half = a.tile_tokens >> 1, my_i = row / a.G, my_hg = row - my_i * a.G, my_tok = w * half + my_i;
   auto row_in = [&](const Segment &g) { return my_i < half && g.tok + my_tok < g.end; };
   SegmentReader<C> rd;
-  while (const Segment *sg = ok ? rd.next_warp(sc, a, ok) : nullptr) {
+  while (const Segment *sg = ok ? rd.next(sc, a, ok) : nullptr) {
     const int n = sg->n, ns = sg->ns;
     const int lim = row_in(*sg) ? (a.causal ? min(max(sg->lim0 + my_tok, 0), sg->L) : sg->L) : sg->klim;
     const uint32_t qe = qi + w;
@@ -926,7 +931,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
   if (warp < 4) {
     if (warp == 0) {
       if constexpr (!C::BITS8) {
-        if (lane == 0) tile_producer<C>(sc, a, x, q_smem, ring, &tm_q, &tm_k, &tm_v);
+        tile_producer<C>(sc, a, x, q_smem, ring, &tm_q, &tm_k, &tm_v, lane);
       }
     } else if (warp == 2) {
       tile_scheduler<C>(sc, a, x, lane);
