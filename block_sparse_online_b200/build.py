@@ -22,6 +22,8 @@ LIB = os.path.join(PKG, "libsolattn.so")
 # memory out of range. Same exports; load it explicitly (solattn.load_library(DEBUG_LIB)).
 DEBUG_LIB = os.path.join(PKG, "libsolattn_debug.so")
 SOURCES = ["solattn_api.cu", "dense_api.cu"]
+# The short call path of the binding (host code only).
+FASTCALL = os.path.join(PKG, "_fastcall.so")
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 
 
@@ -48,5 +50,24 @@ def build(verbose: bool = False, extra=(), debug: bool = False) -> str:
     return out
 
 
+def build_fastcall() -> str:
+    """Compile the binding's short call path against the installed torch."""
+    import sysconfig
+
+    from torch.utils import cpp_extension as ext
+    inc = [f"-I{p}" for p in ext.include_paths("cuda") + [sysconfig.get_paths()["include"], INCLUDE]]
+    lib = [x for p in ext.library_paths("cpu") for x in (f"-L{p}", f"-Wl,-rpath,{p}")]
+    import torch
+    cmd = [os.environ.get("CXX") or shutil.which("g++") or "g++", "-O2", "-std=c++17", "-shared", "-fPIC",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}", *inc, "-o", FASTCALL,
+           os.path.join(CSRC, "fastcall.cpp"), *lib, "-lc10", "-lc10_cuda", "-ltorch_cpu", "-ltorch_python"]
+    res = subprocess.run(cmd, capture_output=True, text=True)
+    if res.returncode != 0:
+        raise RuntimeError("g++ failed:\n" + res.stdout + res.stderr)
+    return FASTCALL
+
+
 if __name__ == "__main__":
     print(build(verbose="--verbose" in sys.argv, debug="--debug" in sys.argv))
+    if "--debug" not in sys.argv:
+        print(build_fastcall())

@@ -21,7 +21,7 @@ using namespace solattn;
 constexpr size_t kHeader = 256;  // [4]: status word
 constexpr unsigned long long kTimeoutNs = 2000000000ull;
 constexpr int kMaxSms = 160;     // blocks per SM slot that the workspace provides for
-constexpr int kRowsBlocks1 = 3 * kMaxSms, kRowsBlocks2 = 2 * kMaxSms;
+constexpr int kRowsBlocks1 = rows_blocks(1) * kMaxSms, kRowsBlocks2 = rows_blocks(2) * kMaxSms;
 
 // Workspace: header, one record per block, then maxima and sums, then outputs of the parts.
 struct DenseWs {
@@ -123,7 +123,7 @@ bool may_split(const DenseArgs &a, int blocks, int min_units) {
 template <class QT, int KIND, int D, int NT, bool PAGED>
 int launch_rows(const DenseArgs &a, int sms, cudaStream_t st) {
   using T = RowTiles<8 * NT>;
-  const int blocks = (NT == 1 ? 3 : 2) * sms;
+  const int blocks = rows_blocks(NT) * sms;
   // A block's share is at least two units (256 keys) when the items alone do not fill the launch.
   constexpr int min_units = 2;
   const bool split = may_split<T>(a, blocks, min_units);

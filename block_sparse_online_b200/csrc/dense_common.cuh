@@ -353,33 +353,61 @@ __global__ void __launch_bounds__(256) join_kernel(const DenseArgs a) {
     }
     return;
   }
-  constexpr int TPR = D / 4;  // threads of a row
-  const int e = threadIdx.x % TPR;
-  for (int i = threadIdx.x / TPR; i < ROWS; i += 256 / TPR) {
+  // A warp for each row: lane p reads the maximum and sum of part p, then every lane adds up its columns, several
+  // parts in flight (one part after the other cost 600 cycles for each of them).
+  constexpr int CPL = D / 32;  // columns of a lane
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  for (int i = warp; i < ROWS; i += 8) {
     const int r = blockIdx.y * ROWS + i;
     int tok, g;
     if (!T::row(a, s.n, rec.w, r, tok, g)) continue;
-    float m = -CUDART_INF_F;
-    for (int p = 0; p < parts; ++p) {
+    float m = -CUDART_INF_F, l = 0.f, o[CPL];
+#pragma unroll
+    for (int e = 0; e < CPL; ++e) o[e] = 0.f;
+    for (int p0 = 0; p0 < parts; p0 += 32) {
+      const int p = p0 + lane;
       const size_t sl = p == 0 ? 2 * c + 1 : 2 * (c + p);
-      m = fmaxf(m, a.part_ml[sl * 2 * T::RT + r]);
-    }
-    float l = 0.f, o0 = 0.f, o1 = 0.f, o2 = 0.f, o3 = 0.f;
-    const float ms = m == -CUDART_INF_F ? 0.f : m;
-    for (int p = 0; p < parts; ++p) {
-      const size_t sl = p == 0 ? 2 * c + 1 : 2 * (c + p);
-      const float w = ex2_approx(a.part_ml[sl * 2 * T::RT + r] - ms);
-      l = fmaf(w, a.part_ml[sl * 2 * T::RT + T::RT + r], l);
-      const float4 x = *reinterpret_cast<const float4 *>(a.part_o + (sl * T::RT + r) * D + 4 * e);
-      o0 = fmaf(w, x.x, o0);
-      o1 = fmaf(w, x.y, o1);
-      o2 = fmaf(w, x.z, o2);
-      o3 = fmaf(w, x.w, o3);
+      const bool in = p < parts;
+      const float mp = in ? a.part_ml[sl * 2 * T::RT + r] : -CUDART_INF_F;
+      float lp = in ? a.part_ml[sl * 2 * T::RT + T::RT + r] : 0.f;
+      float mx = mp;
+#pragma unroll
+      for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+      const float mn = fmaxf(m, mx), ms = mn == -CUDART_INF_F ? 0.f : mn;
+      const float old = ex2_approx(m - ms), w = ex2_approx(mp - ms);  // (0 for -infinity)
+      lp *= w;
+#pragma unroll
+      for (int off = 16; off; off >>= 1) lp += __shfl_xor_sync(0xffffffffu, lp, off);
+      l = fmaf(l, old, lp);
+#pragma unroll
+      for (int e = 0; e < CPL; ++e) o[e] *= old;
+      m = mn;
+      const int np = min(32, parts - p0);
+#pragma unroll 8
+      for (int q = 0; q < np; ++q) {
+        const float wq = __shfl_sync(0xffffffffu, w, q);
+        const size_t sq = p0 + q == 0 ? 2 * c + 1 : 2 * (c + p0 + q);
+        const float *src = a.part_o + (sq * T::RT + r) * D + CPL * lane;
+        if constexpr (CPL == 4) {
+          const float4 x = *reinterpret_cast<const float4 *>(src);
+          o[0] = fmaf(wq, x.x, o[0]);
+          o[1] = fmaf(wq, x.y, o[1]);
+          o[2] = fmaf(wq, x.z, o[2]);
+          o[3] = fmaf(wq, x.w, o[3]);
+        } else {
+          const float2 x = *reinterpret_cast<const float2 *>(src);
+          o[0] = fmaf(wq, x.x, o[0]);
+          o[1] = fmaf(wq, x.y, o[1]);
+        }
+      }
     }
     const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees no key is zero
     QT *dst = static_cast<QT *>(a.out) + rec.y * a.o_batch + static_cast<long long>(s.tok0 + tok) * a.o_tok +
-              static_cast<long long>(rec.z * a.G + g) * a.o_head + 4 * e;
-    *reinterpret_cast<uint2 *>(dst) = make_uint2(pack16<QT>(o0 * inv, o1 * inv), pack16<QT>(o2 * inv, o3 * inv));
+              static_cast<long long>(rec.z * a.G + g) * a.o_head + CPL * lane;
+    if constexpr (CPL == 4)
+      *reinterpret_cast<uint2 *>(dst) = make_uint2(pack16<QT>(o[0] * inv, o[1] * inv), pack16<QT>(o[2] * inv, o[3] * inv));
+    else
+      *reinterpret_cast<uint32_t *>(dst) = pack16<QT>(o[0] * inv, o[1] * inv);
   }
 }
 

@@ -101,6 +101,9 @@ __device__ __forceinline__ uint32_t code_word(uint32_t x) {
 constexpr int kRowsWarps = 4;
 constexpr float kRowsSlack = 8.0f;  // log2 units the reference maximum may lag
 
+// Blocks of an SM, as registers allow (four for the 8-bit kinds spill: 156 against 142 us at 118800 e4m3 keys of 24 heads).
+constexpr int rows_blocks(int nt) { return nt == 1 ? 3 : 2; }
+
 template <class QT, int KIND, int D, int NT, bool PAGED>
 struct RowsCfg {
   static constexpr int ROWS = 8 * NT;
@@ -117,7 +120,7 @@ struct RowsSmem {
 };
 
 template <class QT, int KIND, int D, int NT, bool PAGED>
-__global__ void __launch_bounds__(kRowsWarps * 32, NT == 1 ? 3 : 2) rows_kernel(const __grid_constant__ DenseArgs a, int min_units, int whole_items) {
+__global__ void __launch_bounds__(kRowsWarps * 32, rows_blocks(NT)) rows_kernel(const __grid_constant__ DenseArgs a, int min_units, int whole_items) {
   using C = RowsCfg<QT, KIND, D, NT, PAGED>;
   using T = RowTiles<C::ROWS>;
   using MT = typename std::conditional<KIND == kKind16, QT, __half>::type;  // operands' type

@@ -134,8 +134,19 @@ def _load(path=_LIB_PATH):
     return lib
 
 
+def _addresses(lib):
+    """Addresses of the entry points that the short call path (csrc/fastcall.cpp) calls."""
+    return {n: ctypes.cast(getattr(lib, n), ctypes.c_void_p).value
+            for n in ("solattn_cross", "solattn_paged_forward", "solattn_cache_append", "solattn_cache_read")}
+
+
 _lib = _load()
 _lib_path = _LIB_PATH
+_at = _addresses(_lib)
+try:  # host code only: without it the same calls go through ctypes
+    from . import _fastcall as _fast
+except ImportError:
+    _fast = None
 
 
 def library_path() -> str:
@@ -145,10 +156,10 @@ def library_path() -> str:
 def load_library(path: str = _LIB_PATH) -> str:
     """Route every call of this module through the library at `path` (the release build by
     default, or DEBUG_LIB_PATH); returns the path that was active before."""
-    global _lib, _lib_path
+    global _lib, _lib_path, _at
     lib = _load(path)
     prev = _lib_path
-    _lib, _lib_path = lib, path
+    _lib, _lib_path, _at = lib, path, _addresses(lib)
     return prev
 
 
@@ -596,6 +607,12 @@ def solattn_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_len: to
     may hold anything); a sequence of none gives zeros. H is a multiple of Hkv: query head h
     uses key head h // (H // Hkv). Returns out [B, H, Nq, d]. Asynchronous on ``stream``;
     lengths outside [0, Nk] are reported by :func:`solattn_get_status` on the workspace."""
+    if stream is None and _fast is not None:
+        rc = _fast.cross(_at["solattn_cross"], q, k, v, key_len, out, workspace)
+        if rc is not None:
+            if rc:
+                _check(rc, "solattn_cross")
+            return out
     dt = DTYPES.get(getattr(q, "dtype", None))
     if dt is None or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a bfloat16 or float16 [B, H, N, d] CUDA tensor")
@@ -643,6 +660,8 @@ class PagedCache:
         self.num_pages, self.Hkv, self.page, self.d, self.dtype, self.device = P, Hkv, page, d, dt, dev
         self._c = _Cache(k, v, None if k_scale is None else k_scale.data_ptr(),
                          None if v_scale is None else v_scale.data_ptr(), P, Hkv, page, d, CACHE_KINDS.get(dt, 0))
+        # for the short call path: the structure's address, the device and the 16-bit dtype (or -1)
+        self._fast = (ctypes.addressof(self._c), dev.index, DTYPES.get(dt, -1))
 
     def _seqs(self, table, cu, length, total):
         """The sequences of a call, checked."""
@@ -682,6 +701,12 @@ def solattn_paged_forward(q: torch.Tensor, cache: PagedCache, table: torch.Tenso
     Lengths or pages out of range are reported by :func:`solattn_get_status` on the workspace."""
     if not isinstance(cache, PagedCache):
         raise ValueError("cache must be a PagedCache")
+    if stream is None and _fast is not None:
+        rc = _fast.paged(_at["solattn_paged_forward"], *cache._fast, q, table, cu, length, max_new, causal, out, workspace)
+        if rc is not None:
+            if rc:
+                _check(rc, "solattn_paged_forward")
+            return out
     dtype, total = cache._rows_dtype(q, "q")
     dev, H = cache.device, q.shape[1]
     shape = (total, H, cache.d)
@@ -703,6 +728,12 @@ def solattn_cache_append(cache: PagedCache, new_k: torch.Tensor, new_v: torch.Te
     quantised where the cache is 8-bit: scale = max|x| / TOP, code = nearest(x TOP / max|x|), TOP = 127
     (int8) or 448 (e4m3). table, cu, length as in :func:`solattn_paged_forward` (length counts
     the new tokens). ``workspace``: an :func:`alloc_status` tensor or any workspace."""
+    if stream is None and _fast is not None:
+        rc = _fast.cache_rows(_at["solattn_cache_append"], True, *cache._fast, new_k, new_v, table, cu, length, workspace)
+        if rc is not None:
+            if rc:
+                _check(rc, "solattn_cache_append")
+            return
     dtype, total = cache._rows_dtype(new_k, "new_k")
     dev, shape = cache.device, (total, cache.Hkv, cache.d)
     seqs = cache._seqs(table, cu, length, total)
@@ -716,6 +747,12 @@ def solattn_cache_read(cache: PagedCache, table: torch.Tensor, cu: torch.Tensor,
                        k_out: torch.Tensor, v_out: torch.Tensor, workspace: torch.Tensor | None = None, stream=None):
     """Reads the new tokens' rows (the last cu[b+1] - cu[b] of each sequence) back from the pages into
     k_out and v_out [total, Hkv, d] (bf16 or fp16): code * scale, rounded once. Returns them."""
+    if stream is None and _fast is not None:
+        rc = _fast.cache_rows(_at["solattn_cache_read"], False, *cache._fast, k_out, v_out, table, cu, length, workspace)
+        if rc is not None:
+            if rc:
+                _check(rc, "solattn_cache_read")
+            return k_out, v_out
     dtype, total = cache._rows_dtype(k_out, "k_out")
     dev, shape = cache.device, (total, cache.Hkv, cache.d)
     seqs = cache._seqs(table, cu, length, total)

@@ -456,3 +456,44 @@ def test_explicit_stream_and_two_at_once():
     for x, o in zip(xs, outs):
         want, bound = du.cross_oracle(*x, None, BF)
         du.check(o, want, bound)
+
+
+def test_short_call_path_agrees_with_the_long_one(monkeypatch):
+    """The binding's short call path (every tensor given, current stream) and the Python way make the same call."""
+    g = gen(81)
+    q, k, v = rnd(g, 2, 4, 300, 64), rnd(g, 2, 2, 90, 64), rnd(g, 2, 2, 90, 64)
+    ws = solattn.alloc_cross_workspace(2, 4, 2, 300, 90, 64)
+    kp, vp, ks, vs, table = du.make_cache(g, [70, 33], 2, 16, 64, BF, E4)
+    cache = solattn.PagedCache(kp, vp, ks, vs)
+    pq, new = rnd(g, 5, 4, 64), rnd(g, 5, 2, 64)
+    cu, length = du.cu_of([2, 3]), du.ints([70, 33])
+    pws = solattn.alloc_paged_workspace(cache, 2, 4, 5)
+
+    def calls():
+        out, po = torch.empty_like(q), torch.empty_like(pq)
+        rows = torch.empty_like(new), torch.empty_like(new)
+        solattn.solattn_cross(q, k, v, key_len=du.ints([90, 7]), out=out, workspace=ws)
+        solattn.solattn_cache_append(cache, new, new, table, cu, length, workspace=pws)
+        solattn.solattn_paged_forward(pq, cache, table, cu, length, max_new=3, causal=True, out=po, workspace=pws)
+        solattn.solattn_cache_read(cache, table, cu, length, *rows, workspace=pws)
+        return out, po, *rows
+
+    short = calls()
+    monkeypatch.setattr(solattn, "_fast", None)
+    for a, b in zip(short, calls()):
+        assert torch.equal(a, b)
+    monkeypatch.undo()
+    # what the short path does not take is refused in words
+    bad = torch.empty(2, 4, 300, 64, device="cuda")
+    with pytest.raises(ValueError):
+        solattn.solattn_cross(q, k, v, out=bad, workspace=ws)
+    with pytest.raises(ValueError):
+        solattn.solattn_cross(q, k, v[:, :, :50], out=torch.empty_like(q), workspace=ws)
+    with pytest.raises(solattn.SolAttnError):
+        solattn.solattn_cross(q, k, v, out=torch.empty_like(q), workspace=ws[:512])
+    with pytest.raises(ValueError):
+        solattn.solattn_paged_forward(pq, cache, table.long(), cu, length, max_new=1, out=torch.empty_like(pq), workspace=pws)
+    with pytest.raises(ValueError):
+        solattn.solattn_paged_forward(pq, cache, table, cu[:2], length, max_new=1, out=torch.empty_like(pq), workspace=pws)
+    with pytest.raises(solattn.SolAttnError):
+        solattn.solattn_paged_forward(pq, cache, table, cu, length, max_new=-1, out=torch.empty_like(pq), workspace=pws)
