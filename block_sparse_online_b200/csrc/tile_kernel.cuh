@@ -53,8 +53,10 @@ struct TileCfg {
   static constexpr int HALF_BYTES = 128 * D * 2;  // a half's queries, or a unit of K or V
   // 224 KB of tiles at d = 128: 3 + 4 (16-bit), 2 + 4 (8-bit, which also keeps scales)
   static constexpr int NQ = BITS8 ? 2 : 3;
-  static constexpr int NSLOT = D == 128 ? 4 : 8;
-  static constexpr int NSC = 4;  // units whose scales are kept
+  static constexpr int NSLOT = D == 128 ? 4 : 8;  // even: K in the even slots, V in the odd ones
+  // Units whose scales are kept. A unit's slot of K is free as soon as its last S is there, while the softmax still
+  // reads its scales: the converter may be NSLOT / 2 units ahead of the last unit that is done with.
+  static constexpr int NSC = NSLOT / 2 + 2;
   static constexpr int COLS = 128 + D;  // tensor memory columns of a half: O, two buffers of S (and P)
   static constexpr int TMEM_COLS = 512;
   static constexpr int THREADS = BITS8 ? 512 : 384;
@@ -311,24 +313,34 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
     return w;
   };
   uint4 ck[NP], cv[NP];  // codes of the next unit's keys and values
+  uint32_t there = 0;    // which of them exist
   float ksc, vsc;
-  // Pages of a unit: lane g holds that of its keys 16 (g % 8) .. + 15 (a page has 16 tokens at least), or -1
-  // behind the sequence's end and for bad entries. Looked up a unit ahead of the codes: a lookup
-  // before each row's load took 2300 cycles for a unit's keys.
-  auto fetch_pages = [&](const Segment &c, int u) {
+  // Table entries of a unit: lane g holds that of its keys 16 (g % 8) .. + 15 (a page has 16 tokens at least), or -2
+  // behind the sequence's end. Read a unit ahead of the codes, and looked at only then.
+  auto fetch_entries = [&](const Segment &c, int u) {
     const int j = u * kUnitKeys + (lane & 7) * 16;
-    return j < c.L ? page_of(a, c.b, j) : -1;
+    return j < c.L ? __ldg(a.table + static_cast<size_t>(c.b) * a.width + (j >> a.page_shift)) : -2;
   };
-  // Codes of a unit's keys or values into registers.
+  // The pages they name; -1 for none (an entry that names no page of the cache is recorded).
+  auto pages_of = [&](int entry) {
+    if (static_cast<unsigned>(entry) < static_cast<unsigned>(a.num_pages)) return entry;
+    if (entry != -2) atomicCAS(a.status, 0, kStatusTable);
+    return -1;
+  };
+  // Codes of a unit's keys or values into registers; bit i of the result: pass i has a key there (the others read
+  // some row of page 0, without a branch, and are zeroed later).
   auto fetch = [&](const Segment &c, int u, int pages, bool is_v, uint4(&cd)[NP]) {
     const uint8_t *base = static_cast<const uint8_t *>(is_v ? a.v : a.k) + c.h * (is_v ? a.v_head : a.k_head) + pc * 16;
     const long long row = is_v ? a.v_row : a.k_row, seq = is_v ? a.v_seq : a.k_seq;
+    uint32_t there = 0;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int j = u * kUnitKeys + i * RPP + rl;
       const int id = __shfl_sync(0xffffffffu, pages, (i * RPP + rl) >> 4);
-      cd[i] = id >= 0 && j < c.L ? ld_stream16(base + id * seq + (j & (a.page - 1)) * row) : make_uint4(0, 0, 0, 0);
+      there |= (id >= 0 && j < c.L ? 1u : 0u) << i;
+      cd[i] = ld_stream16(base + max(id, 0) * seq + (j & (a.page - 1)) * row);
     }
+    return there;
   };
   // The scales of a unit: thread t takes key t.
   auto fetch_scales = [&](const Segment &c, int u, int pages) {
@@ -339,12 +351,13 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
     ksc = in ? __ldg(a.k_scale + at) : 0.f;
     vsc = in ? __ldg(a.v_scale + at) : 0.f;
   };
-  auto expand = [&](uint8_t *dst, const uint4(&cd)[NP]) {
+  auto expand = [&](uint8_t *dst, const uint4(&cd)[NP], uint32_t there) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int r = i * RPP + rl;
       uint32_t w[8];
-      const uint32_t cw[4] = {cd[i].x, cd[i].y, cd[i].z, cd[i].w};
+      const bool in = (there >> i) & 1u;
+      const uint32_t cw[4] = {in ? cd[i].x : 0u, in ? cd[i].y : 0u, in ? cd[i].z : 0u, in ? cd[i].w : 0u};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t t = code_word<C::KIND>(cw[e]);
@@ -366,8 +379,8 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
   SegmentReader<C> rd;
   const Segment *g = rd.next(sc, a, ok);
   if (g) {
-    const int pages = fetch_pages(*g, g->u0);
-    fetch(*g, g->u0, pages, false, ck);
+    const int pages = pages_of(fetch_entries(*g, g->u0));
+    there = fetch(*g, g->u0, pages, false, ck);
     fetch_scales(*g, g->u0, pages);
     fetch(*g, g->u0, pages, true, cv);
   }
@@ -447,7 +460,7 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
         f = nxt = rd.next(sc, a, ok);
         if (f) fu = f->u0;
       }
-      const int pages = f ? fetch_pages(*f, fu) : -1;
+      const int entries = f ? fetch_entries(*f, fu) : -2;
       int sl = kv % C::NSLOT;
       if (!wait(&sc.empty[sl], ((kv / C::NSLOT) & 1) ^ 1)) break;
       // scales: the reference is a power of two >= the largest value scale so far (2^-100 .. 2^100)
@@ -473,16 +486,18 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
       sc.vs[ss][tid] = vref > 0.f ? vsc * __int_as_float((254 << 23) - __float_as_int(vref)) : vsc;
       if (tid == 0) sc.vgrow[ss] = growth, sc.vref[ss] = vref;
       ++tile;
-      expand(ring + sl * C::HALF_BYTES, ck);
+      expand(ring + sl * C::HALF_BYTES, ck, there);
       publish(&sc.full[sl]);
       ++kv;
+      const uint32_t there_v = there;
+      const int pages = pages_of(entries);
       if (f) {
-        fetch(*f, fu, pages, false, ck);
+        there = fetch(*f, fu, pages, false, ck);
         fetch_scales(*f, fu, pages);
       }
       sl = kv % C::NSLOT;
       if (!wait(&sc.empty[sl], ((kv / C::NSLOT) & 1) ^ 1)) break;
-      expand(ring + sl * C::HALF_BYTES, cv);
+      expand(ring + sl * C::HALF_BYTES, cv, there_v);
       publish(&sc.full[sl]);
       ++kv;
       if (f) fetch(*f, fu, pages, true, cv);
@@ -645,10 +660,10 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
       tmem_ld32(s_addr + 32, *reinterpret_cast<uint32_t(*)[32]>(x + 32));
       // The group that produced this S is complete, so this half has done with K of the unit (after its
       // last step), with V of the unit that ended two steps ago, and after the last S with its queries.
-      if (leader) {
-        if (b == 1 || j == ns - 1) release(kv + (j & ~1));
-        if (b == 1 && j >= 3) release(kv + j - 2);
-      }
+      // (8-bit keys: each warp speaks for itself about K, whose barrier it has just waited on: once the slot is refilled
+      // that wait could no longer tell the phases apart)
+      if ((C::BITS8 ? lane == 0 : leader) && (b == 1 || j == ns - 1)) release(kv + (j & ~1));
+      if (leader && b == 1 && j >= 3) release(kv + j - 2);
       const int base = sg->u0 * kUnitKeys + j * kStepKeys;
       const int left = lim - base;  // keys of this step that the row sees
       float alpha = 1.f, lsum = 0.f;
@@ -877,7 +892,7 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     const int fillers = C::BITS8 ? 128 : 1;  // converter threads, or the producer's expected bytes
     for (int i = 0; i < C::NSLOT; ++i) {
       mbar_init(&sc.full[i], fillers);
-      mbar_init(&sc.empty[i], 2);  // one arrival per half
+      mbar_init(&sc.empty[i], C::BITS8 && i % 2 == 0 ? 8 : 2);  // an arrival per half, or (K in the even slots) per softmax warp
     }
     for (int i = 0; i < C::NQ; ++i) {
       mbar_init(&sc.q_full[i], fillers);

@@ -497,3 +497,24 @@ def test_short_call_path_agrees_with_the_long_one(monkeypatch):
         solattn.solattn_paged_forward(pq, cache, table, cu[:2], length, max_new=1, out=torch.empty_like(pq), workspace=pws)
     with pytest.raises(solattn.SolAttnError):
         solattn.solattn_paged_forward(pq, cache, table, cu, length, max_new=-1, out=torch.empty_like(pq), workspace=pws)
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("kind", [None, I8, E4], ids=["16", "int8", "e4m3"])
+def test_repeated_passes_agree(d, kind):
+    """Many passes of a batch of chunks give the same bits: no buffer is overwritten before it has been read."""
+    g, H, Hkv, page = gen(91), 8, 4, 32
+    ns, lens = [700, 1300, 65, 1], [1500, 4400, 700, 2000]
+    k, v, ks, vs, table = du.make_cache(g, lens, Hkv, page, d, BF, kind)
+    cache = solattn.PagedCache(k, v, ks, vs)
+    q = rnd(g, sum(ns), H, d)
+    cu, length = du.cu_of(ns), du.ints(lens)
+    ws = solattn.alloc_paged_workspace(cache, len(ns), H, sum(ns))
+    outs = [torch.empty_like(q) for _ in range(2)]
+    solattn.solattn_paged_forward(q, cache, table, cu, length, max_new=1300, causal=False, out=outs[0], workspace=ws)
+    for _ in range(60):
+        solattn.solattn_paged_forward(q, cache, table, cu, length, max_new=1300, causal=False, out=outs[1], workspace=ws)
+        assert torch.equal(outs[0], outs[1])
+    assert solattn.solattn_get_status(ws) == 0
+    want, bound = du.paged_oracle(q, k, v, ks, vs, table, ns, lens, False, BF)
+    du.check(outs[1], want, bound)
