@@ -313,7 +313,6 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
     return w;
   };
   uint4 ck[NP], cv[NP];  // codes of the next unit's keys and values
-  uint32_t there = 0;    // which of them exist
   float ksc, vsc;
   // Table entries of a unit: lane g holds that of its keys 16 (g % 8) .. + 15 (a page has 16 tokens at least), or -2
   // behind the sequence's end. Read a unit ahead of the codes, and looked at only then.
@@ -327,20 +326,16 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
     if (entry != -2) atomicCAS(a.status, 0, kStatusTable);
     return -1;
   };
-  // Codes of a unit's keys or values into registers; bit i of the result: pass i has a key there (the others read
-  // some row of page 0, without a branch, and are zeroed later).
+  // Codes of a unit's keys or values into registers, zeros where there is no key.
   auto fetch = [&](const Segment &c, int u, int pages, bool is_v, uint4(&cd)[NP]) {
     const uint8_t *base = static_cast<const uint8_t *>(is_v ? a.v : a.k) + c.h * (is_v ? a.v_head : a.k_head) + pc * 16;
     const long long row = is_v ? a.v_row : a.k_row, seq = is_v ? a.v_seq : a.k_seq;
-    uint32_t there = 0;
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int j = u * kUnitKeys + i * RPP + rl;
       const int id = __shfl_sync(0xffffffffu, pages, (i * RPP + rl) >> 4);
-      there |= (id >= 0 && j < c.L ? 1u : 0u) << i;
-      cd[i] = ld_stream16(base + max(id, 0) * seq + (j & (a.page - 1)) * row);
+      cd[i] = id >= 0 && j < c.L ? ld_stream16(base + id * seq + (j & (a.page - 1)) * row) : make_uint4(0, 0, 0, 0);
     }
-    return there;
   };
   // The scales of a unit: thread t takes key t.
   auto fetch_scales = [&](const Segment &c, int u, int pages) {
@@ -351,13 +346,12 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
     ksc = in ? __ldg(a.k_scale + at) : 0.f;
     vsc = in ? __ldg(a.v_scale + at) : 0.f;
   };
-  auto expand = [&](uint8_t *dst, const uint4(&cd)[NP], uint32_t there) {
+  auto expand = [&](uint8_t *dst, const uint4(&cd)[NP]) {
 #pragma unroll
     for (int i = 0; i < NP; ++i) {
       const int r = i * RPP + rl;
       uint32_t w[8];
-      const bool in = (there >> i) & 1u;
-      const uint32_t cw[4] = {in ? cd[i].x : 0u, in ? cd[i].y : 0u, in ? cd[i].z : 0u, in ? cd[i].w : 0u};
+      const uint32_t cw[4] = {cd[i].x, cd[i].y, cd[i].z, cd[i].w};
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const uint32_t t = code_word<C::KIND>(cw[e]);
@@ -380,7 +374,7 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
   const Segment *g = rd.next(sc, a, ok);
   if (g) {
     const int pages = pages_of(fetch_entries(*g, g->u0));
-    there = fetch(*g, g->u0, pages, false, ck);
+    fetch(*g, g->u0, pages, false, ck);
     fetch_scales(*g, g->u0, pages);
     fetch(*g, g->u0, pages, true, cv);
   }
@@ -486,18 +480,17 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
       sc.vs[ss][tid] = vref > 0.f ? vsc * __int_as_float((254 << 23) - __float_as_int(vref)) : vsc;
       if (tid == 0) sc.vgrow[ss] = growth, sc.vref[ss] = vref;
       ++tile;
-      expand(ring + sl * C::HALF_BYTES, ck, there);
+      expand(ring + sl * C::HALF_BYTES, ck);
       publish(&sc.full[sl]);
       ++kv;
-      const uint32_t there_v = there;
       const int pages = pages_of(entries);
       if (f) {
-        there = fetch(*f, fu, pages, false, ck);
+        fetch(*f, fu, pages, false, ck);
         fetch_scales(*f, fu, pages);
       }
       sl = kv % C::NSLOT;
       if (!wait(&sc.empty[sl], ((kv / C::NSLOT) & 1) ^ 1)) break;
-      expand(ring + sl * C::HALF_BYTES, cv, there_v);
+      expand(ring + sl * C::HALF_BYTES, cv);
       publish(&sc.full[sl]);
       ++kv;
       if (f) fetch(*f, fu, pages, true, cv);
