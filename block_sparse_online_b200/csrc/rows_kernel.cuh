@@ -16,9 +16,9 @@
 //
 // Softmax: a row's reference maximum moves only when a score exceeds it by more than 8 (in
 // log2 units), so the usual step has one vote in place of the shuffles of a maximum, and
-// P <= 2^8. P is rounded to the 16-bit type of the product (bf16 or fp16, relative 2^-9 or
-// 2^-12 on average less; independent over the keys, so it averages out below the output's own
-// rounding); maxima, sums and O stay in 32 bits.
+// P <= 2^8. P is rounded to the 16-bit type of the product: off by at most 2^-8 (bf16) or 2^-11
+// (fp16) of each value, independently from key to key, which adds about as much to the result's
+// error as the output's own rounding. Maxima, sums and O stay in 32 bits.
 //
 // 8-bit caches: codes are expanded to fp16 (exact: int8 has 8 bits, e4m3 four and a range
 // that fp16 holds). A key's scale multiplies its score in 32 bits. A value's scale
@@ -26,6 +26,11 @@
 // largest value scale met so far (exact; O follows when it grows), so the product stays in
 // fp16's range for caches of any magnitude. Queries in bf16 become fp16 after a division of each row
 // by a power of two that brings its largest element to [2^14, 2^15): exact down to 2^-31 of that element.
+//
+// Bound by memory: at 32 sequences of 1 to 16384 keys, 4 key heads of 128, bf16, one token each, it reads
+// 551 MB in 85.5 us (6.4 TB/s). In e4m3 at 118800 keys of 24 heads (753 MB) it takes 141 us (5.3 TB/s): half the
+// bytes for each key leave half the bytes in flight, and more blocks per SM cost spills. Measured and not kept:
+// the next values loaded before the next scores (155 us there), four blocks per SM (156 us).
 #pragma once
 
 #include "dense_common.cuh"

@@ -6,10 +6,9 @@
 // once per 256 rows. Roles, by warp:
 //   warp 0       16-bit keys: TMA producer. Q halves into three buffers (the next item's first half
 //                lands while this item runs), K and V units into a ring.
-//   warps 1, 3   MMA issuers, one thread for each half: S = Q K^T into tensor memory, O += P V with
-//                P read from tensor memory. They take turns through a shared counter, as the
-//                issuers of the sparse kernel do, so the tensor core works on one half while the
-//                other half's softmax runs.
+//   warps 1, 3   MMA issuers, one for each half: S = Q K^T into tensor memory, O += P V with
+//                P read from tensor memory. They take turns through a shared counter, so the tensor core
+//                works on one half while the other half's softmax runs.
 //   warp 2       owns the TMEM allocation; walks the block's range of the line and publishes its
 //                segments (one tile's run of units) to the other roles, a few ahead.
 //   warps 4-11   softmax, one warpgroup for each half, one row per thread. Where a sequence ends inside a step they
@@ -18,16 +17,24 @@
 //                queries, scaled, into their buffers), one unit ahead in registers.
 // A step is 64 keys. Each half has two buffers of S (P takes the place of its S): Q K^T of step j + 2
 // follows P V of step j, so while a warpgroup exponentiates step j + 1 the tensor core works on its steps
-// j and j + 2. With one buffer of 128 keys instead, S, softmax and P V formed one chain of 3700 cycles a
-// unit (the tensor core needs 2048 for both halves).
+// j and j + 2. With one buffer of 128 keys instead, S, softmax and P V form one chain of 3500 to 3700 cycles a
+// unit for both halves, of which the tensor core works 2130.
 //
-// Softmax: once a row has a reference maximum a unit is exponentiated against it without taking the row
-// maximum; a row sum <= 2^15 shows that no value is large, otherwise (or for a row's first
-// unit) the maximum is taken and the unit done again. P is rounded to the 16-bit type of the
-// keys (bf16: half a step of 2^-9 on average; independent from key to key, so the output's
-// own rounding is what remains; fp16 for 8-bit caches). The reference, sums and O are in 32 bits.
-// One pair of exponentials in kTilePolyEvery goes through the polynomial on the FMA pipe;
-// a unit that is done again uses the special-function unit only, which hands NaN through.
+// Softmax: once a row has a reference maximum a step is exponentiated against it without taking the row
+// maximum; a row sum <= 2^15 shows that no value is large, otherwise (or for a row's first step, or a masked
+// one) the maximum is taken (a NaN wins it) and the step done again. P is rounded to the 16-bit type of the
+// keys, fp16 for 8-bit caches: off by at most 2^-8 (bf16) or 2^-11 of each value, independently from key to
+// key, which adds about as much to the result's error as the output's own rounding. The reference, sums and
+// O are in 32 bits. Two pairs of exponentials in eight go through the polynomial on the FMA pipe.
+//
+// What bounds it, measured at 1560 tokens x 32760 keys x 12 heads of 128 in bf16 (350 to 400 us, 800 to 900
+// TFLOP/s; the card's power limit moves it): the tensor core's instructions. A step's 8 products of 64 columns
+// take 85 cycles each where 128 columns take 67, so a step costs both halves 1900 cycles, the
+// softmax 1700. Measured and not kept: one S buffer of 128 columns with two warpgroups a half by columns
+// (387 us), two warpgroups a half by steps (400 us), output by TMA stores (no gain, and the queries'
+// buffer comes back late), a deeper queue of queries for a shallower ring of keys (558 us). Short rows of
+// keys (one or two steps) are bound by a tile's fixed 5500 cycles: queries in, first maximum, rows out.
+// 8-bit caches add the expansion of the codes, which is what bounds them (536 us for the same in int8).
 //
 // Causal and ragged ends: columns at or behind a row's limit are replaced by -infinity; the
 // products of a unit stop at the last 16 keys that some row of the tile sees.
@@ -40,7 +47,8 @@ namespace solattn {
 
 constexpr float kTileSlack = 8.0f;         // log2 units the reference may lag a unit's maximum
 constexpr float kTileSumLimit = 32768.0f;  // row sum that shows every value <= 2^15
-constexpr uint32_t kTilePolyMask = 0x88u;  // pairs (mod 8) on the polynomial
+// Pairs (mod 8) on the polynomial: at 1560 x 32760 none 416, one 384, two 359, three 390 us.
+constexpr uint32_t kTilePolyMask = 0x88u;
 
 template <class QT_, int KIND_, int D_, bool PAGED_>
 struct TileCfg {
