@@ -199,7 +199,7 @@ def test_paged_magnitudes(n, kind, mul, qmul):
     run_paged([n, n], [999, 257], 4, 2, 32, 128, True, BF, kind, mul=mul, qmul=qmul)
 
 
-@pytest.mark.parametrize("n", [1, 150])
+@pytest.mark.parametrize("n", [1, 150, 400])
 def test_paged_8bit_scales_far_apart(n):
     """Value scales that grow along the sequence by many orders, and rows of zeros among them."""
     g, d, page, L = gen(21), 128, 16, 700
@@ -217,15 +217,16 @@ def test_paged_8bit_scales_far_apart(n):
     du.check(out, want, bound)
 
 
-@pytest.mark.parametrize("n", [1, 300])
-def test_paged_bad_pages_read_as_zeros(n):
+@pytest.mark.parametrize("n,H", [(1, 2), (300, 2), (400, 32)])
+@pytest.mark.parametrize("kind", [None, I8], ids=["16", "int8"])
+def test_paged_bad_pages_read_as_zeros(n, H, kind):
     g, d, page, L = gen(31), 64, 16, 400
-    k, v, ks, vs, table = du.make_cache(g, [L], 2, page, d, BF, None)
+    k, v, ks, vs, table = du.make_cache(g, [L], 2, page, d, BF, kind)
     bad = table.clone()
     bad[0, 3], bad[0, 7] = -5, 1 << 20
-    q = rnd(g, n, 2, d)
-    cache = solattn.PagedCache(k, v)
-    ws = solattn.alloc_paged_workspace(cache, 1, 2, n)
+    q = rnd(g, n, H, d)
+    cache = solattn.PagedCache(k, v, ks, vs)
+    ws = solattn.alloc_paged_workspace(cache, 1, H, n)
     out = solattn.solattn_paged_forward(q, cache, bad, du.cu_of([n]), du.ints([L]), max_new=n, causal=False, workspace=ws)
     assert solattn.solattn_get_status(ws) == solattn.SOLATTN_ETABLE
     for p in (3, 7):
@@ -324,7 +325,7 @@ def test_cross(case, dtype, layout):
     du.check(out, want, bound)
 
 
-@pytest.mark.parametrize("Nq", [3, 200])
+@pytest.mark.parametrize("Nq", [3, 200, 2000])
 def test_cross_broadcast_and_slices(Nq):
     """Keys expanded over the batch, values cut out of a fused projection, a wide output."""
     g, B, H, Nk, d = gen(8), 3, 2, 190, 128
@@ -349,7 +350,7 @@ def test_cross_bad_lengths_are_cut_and_reported():
     du.check(out, want, bound)
 
 
-@pytest.mark.parametrize("Nq", [4, 400])
+@pytest.mark.parametrize("Nq", [4, 400, 20000])
 def test_masked_infinities_and_nan_in_values(Nq):
     """A NaN among the keys that a row sees reaches that row; a score of -inf is a key without weight."""
     g = gen(12)
@@ -364,6 +365,92 @@ def test_masked_infinities_and_nan_in_values(Nq):
     out = solattn.solattn_cross(q, k, v)
     keep = torch.arange(200, device="cuda") != 150
     want, bound = du.cross_oracle(q, k[:, :, keep], v[:, :, keep], None, BF)
+    du.check(out, want, bound)
+    for at in (0, 70, 199):  # a NaN in a key that every row sees: its scores are NaN, and so are the rows
+        kk = k.clone()
+        kk[0, 0, at, 7] = float("nan")
+        assert solattn.solattn_cross(q, kk, v).isnan().all()
+
+
+# ------------------------------------------------------------------ many rows with every kind of edge
+
+BIG_CROSS = [  # (B, H, Hkv, Nq, Nk, d, lens): enough products for the tile kernel
+    (3, 6, 2, 3000, 200, 64, [200, 0, 13]),
+    (2, 4, 4, 2000, 769, 128, [769, 130]),
+    (4, 8, 8, 2500, 33, 64, [33, 2, 0, 16]),
+    (1, 16, 16, 4097, 77, 128, None),
+    (2, 3, 1, 6333, 128, 128, [128, 64]),
+    (1, 2, 2, 50000, 17, 128, None),
+    (3, 7, 1, 1999, 320, 64, [1, 320, 65]),
+]
+
+
+@pytest.mark.parametrize("case", BIG_CROSS, ids=[str(i) for i in range(len(BIG_CROSS))])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_cross_many_rows(case, dtype):
+    B, H, Hkv, Nq, Nk, d, lens = case
+    g = gen(13)
+    q = rnd(g, B, Nq, H, d, mul=2.0, dtype=dtype).transpose(1, 2)
+    k, v = rnd(g, B, Hkv, Nk, d, dtype=dtype), rnd(g, B, Nk, Hkv, d, dtype=dtype).transpose(1, 2)
+    if lens is not None:
+        for b, L in enumerate(lens):
+            k[b, :, L:] = float("inf")
+            v[b, :, L:] = float("nan")
+    ws = solattn.alloc_cross_workspace(B, H, Hkv, Nq, Nk, d)
+    key_len = None if lens is None else du.ints(lens)
+    out = solattn.solattn_cross(q, k, v, key_len=key_len, workspace=ws)
+    for _ in range(4):
+        assert torch.equal(out, solattn.solattn_cross(q, k, v, key_len=key_len, workspace=ws))
+    assert solattn.solattn_get_status(ws) == 0
+    want, bound = du.cross_oracle(q, k, v, lens, dtype)
+    du.check(out, want, bound)
+
+
+BIG_PAGED = [
+    ([700, 1, 0, 300], [900, 1, 5, 300], 6, 2, 16, 128, True),
+    ([513, 200], [513, 1000], 10, 2, 32, 64, True),
+    ([257, 700], [3000, 700], 5, 5, 128, 64, False),
+    ([2000], [2000], 3, 1, 64, 128, True),
+    ([130] * 9, [130 + 61 * i for i in range(9)], 16, 4, 16, 64, True),
+]
+
+
+@pytest.mark.parametrize("case", BIG_PAGED, ids=[str(i) for i in range(len(BIG_PAGED))])
+@pytest.mark.parametrize("dtype,kind", [(BF, None), (FP, None), (BF, I8), (FP, E4), (BF, E4), (FP, I8)],
+                         ids=["bf16", "fp16", "bf16-int8", "fp16-e4m3", "bf16-e4m3", "fp16-int8"])
+def test_paged_many_rows(case, dtype, kind):
+    run_paged(*case, dtype, kind)
+
+
+@pytest.mark.parametrize("Nq", [30, 3000])
+def test_cross_more_query_heads_than_half_a_tile(Nq):
+    g = gen(14)
+    q, k, v = rnd(g, 1, 130, Nq, 64), rnd(g, 1, 1, 100, 64), rnd(g, 1, 1, 100, 64)
+    want, bound = du.cross_oracle(q, k, v, None, BF)
+    du.check(solattn.solattn_cross(q, k, v), want, bound)
+
+
+def test_more_sequences_than_are_searched_at_once():
+    """1100 sequences, single tokens and none: write, attend, read back."""
+    B, Hkv, H, d, page = 1100, 1, 2, 64, 16
+    ns = [i % 3 != 1 and 1 or 0 for i in range(B)]
+    lens = [max(n, (7 * i) % 40) for i, n in enumerate(ns)]
+    g = gen(15)
+    k, v, ks, vs, table = du.make_cache(g, lens, Hkv, page, d, BF, I8)
+    cache = solattn.PagedCache(k, v, ks, vs)
+    total = sum(ns)
+    new = rnd(g, total, Hkv, d), rnd(g, total, Hkv, d)
+    cu, length = du.cu_of(ns), du.ints(lens)
+    ws = solattn.alloc_paged_workspace(cache, B, H, total)
+    solattn.solattn_cache_append(cache, *new, table, cu, length, workspace=ws)
+    back = solattn.solattn_cache_read(cache, table, cu, length, torch.empty_like(new[0]), torch.empty_like(new[1]), workspace=ws)
+    for x, y in zip(new, back):
+        codes, sc = du.quantise(x, I8)
+        assert torch.equal(y, (codes.float() * sc[..., None]).to(BF))
+    q = rnd(g, total, H, d)
+    out = solattn.solattn_paged_forward(q, cache, table, cu, length, max_new=1, workspace=ws)
+    assert solattn.solattn_get_status(ws) == 0
+    want, bound = du.paged_oracle(q, k, v, ks, vs, table, ns, lens, True, BF)
     du.check(out, want, bound)
 
 
