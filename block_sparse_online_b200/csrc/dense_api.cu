@@ -219,13 +219,33 @@ int launch_tiles(DenseArgs a, int dtype, int sms, cudaStream_t st) {
   return SOLATTN_OK;
 }
 
+// Which kernel is sooner done, by what each costs (us, d = 128): a start, a share for each item of a block, a share for
+// each unit of keys, and the join of split items. Fitted to, rows kernel against tile kernel (B, Hkv, Nq, Nk):
+// (1, 8, 256, 256) 10.4 against 11.9, (1, 8, 1024, 256) 17.2 : 12.3, (1, 8, 2048, 512) 49.6 : 16.4, (2, 8, 32, 4096) 23.3 :
+// 33.2, (1, 8, 128, 2048) 22.4 : 25.3, (4, 16, 1024, 128) 70.4 : 16.4, (1, 1, 100, 4096) 21.6 : 30.7. Over a cache the
+// longest sequence that the table could name stands for all of them.
+bool tiles_faster(const DenseArgs &a, int sms) {
+  const int tile_tokens = 2 * (128 / a.G);
+  auto estimate = [&](double per_head, double blocks, double least, double start, double item, double unit, double join) {
+    const double items = per_head * a.Hkv, units = a.Lmax > 32 ? a.Lmax / 128.0 : 0.25;
+    const double share = items * units / blocks, floor = units < least ? units : least;
+    return start + item * (items > blocks ? items / blocks : 1.0) + unit * (share > floor ? share : floor) +
+           (items < blocks && units > least ? join : 0.0);
+  };
+  const double n = a.cu ? a.total : a.n, copies = a.cu ? 1 : a.B;
+  auto ceil_div = [](double x, double y) { return std::ceil(x / y); };
+  double row_tiles = copies * ceil_div(n * a.G, 16), tiles = copies * ceil_div(n, tile_tokens);
+  if (a.cu) {  // every sequence has a tile of its own
+    row_tiles = row_tiles > a.B ? row_tiles : a.B;
+    tiles = tiles > a.B ? tiles : a.B;
+  }
+  return estimate(tiles, sms, 4, 6.0, 2.9, 1.95, 5.0) < estimate(row_tiles, 2.0 * sms, 2, 5.0, 2.2, 2.4, 3.0);
+}
+
 template <class QT, int KIND, int D, bool PAGED>
 int dispatch_rows(const DenseArgs &a, int dtype, int rows, int sms, cudaStream_t st) {
   constexpr int kind = KIND == kKind16 ? SOLATTN_CACHE_16 : KIND == kKindInt8 ? SOLATTN_CACHE_INT8 : SOLATTN_CACHE_E4M3;
-  // Few rows, or little work: the rows kernel starts faster (6 against 9.5 us at 0.04 GFLOP, 10.4 against
-  // 11.9 us at 0.27) and the tile kernel wins as soon as there are products to do (12 against 17 us at 1.07).
-  const double flops = 4.0 * D * a.Hkv * a.G * static_cast<double>(a.cu ? a.total : static_cast<long long>(a.n) * a.B) * a.Lmax;
-  if (rows > 16 && flops > 4e8 && tile_fits(a, kind)) return launch_tiles<QT, KIND, D, PAGED>(a, dtype, sms, st);
+  if (rows > 16 && tile_fits(a, kind) && tiles_faster(a, sms)) return launch_tiles<QT, KIND, D, PAGED>(a, dtype, sms, st);
   return rows <= 8 ? launch_rows<QT, KIND, D, 1, PAGED>(a, sms, st) : launch_rows<QT, KIND, D, 2, PAGED>(a, sms, st);
 }
 

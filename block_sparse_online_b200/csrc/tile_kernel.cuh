@@ -34,7 +34,7 @@
 // (387 us), two warpgroups a half by steps (400 us), output by TMA stores (no gain, and the queries'
 // buffer comes back late), a deeper queue of queries for a shallower ring of keys (558 us). Short rows of
 // keys (one or two steps) are bound by a tile's fixed 5500 cycles: queries in, first maximum, rows out.
-// 8-bit caches add the expansion of the codes, which is what bounds them (536 us for the same in int8).
+// 8-bit caches add the expansion of the codes, which is what bounds them (540 to 560 us for the same in int8).
 //
 // Causal and ragged ends: columns at or behind a row's limit are replaced by -infinity; the
 // products of a unit stop at the last 16 keys that some row of the tile sees.
