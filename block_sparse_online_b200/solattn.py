@@ -7,6 +7,8 @@ fails loudly if ``libsolattn.so`` has not been built; there is no fallback.
 from __future__ import annotations
 
 import ctypes
+import functools
+import inspect
 import os
 
 import torch
@@ -183,6 +185,30 @@ def _stream(stream, device=None):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+def _on_stream(fn):
+    """For a call with a ``stream`` parameter: what it allocates (workspace, outputs) and clears belongs to
+    the stream it launches on. Memory taken on another stream could be in use there still, and a
+    workspace given back there would be handed out again while the kernels run. Tensors that the call returns
+    are marked as used on the caller's stream too, so that dropping them there is safe."""
+    at = list(inspect.signature(fn).parameters).index("stream")
+
+    @functools.wraps(fn)
+    def call(*args, **kw):
+        stream = args[at] if len(args) > at else kw.get("stream")
+        if stream is None:
+            return fn(*args, **kw)
+        with torch.cuda.stream(stream):
+            result = fn(*args, **kw)
+        caller = torch.cuda.current_stream(stream.device)
+        if caller != stream:
+            for t in result if isinstance(result, tuple) else (result,):
+                if isinstance(t, torch.Tensor) and t.is_cuda:
+                    t.record_stream(caller)
+        return result
+
+    return call
+
+
 def _check_buffer(t, name, dtypes, numel, device):
     """A caller-provided buffer the library writes or reads through a raw pointer: it must
     be contiguous, of an accepted dtype, hold at least ``numel`` elements and live on the
@@ -225,6 +251,7 @@ def alloc_workspace(B, H, N, d, Bq, Bk, device="cuda") -> torch.Tensor:
     return torch.empty(n, dtype=torch.uint8, device=device)
 
 
+@_on_stream
 def solattn_pool(x: torch.Tensor, blk: int, out: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """Block means of a bf16 [B, H, N, d] CUDA tensor -> fp32 [B, H, ceil(N/blk), d]."""
     B, H, N, d = _bhnd(x)
@@ -274,6 +301,7 @@ def _prepare(q, k, v, Bq, Bk, out, kept_per_head, keep_mask, workspace):
     return B, H, N, d, out, kept_per_head, mask, workspace, stats
 
 
+@_on_stream
 def solattn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, Bq: int, Bk: int, tau: float,
                     mode="keep_correct", out: torch.Tensor | None = None,
                     kept_per_head: torch.Tensor | None = None, keep_mask: bool | torch.Tensor = False,
@@ -306,6 +334,7 @@ def solattn_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, Bq: int, 
     return out, kept_per_head, mask
 
 
+@_on_stream
 def solattn_forward_gaussian(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, Bq: int, Bk: int, beta: float,
                              variant="exact", mode="keep_correct", out: torch.Tensor | None = None,
                              kept_per_head: torch.Tensor | None = None, keep_mask: bool | torch.Tensor = False,
@@ -326,6 +355,7 @@ def solattn_forward_gaussian(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, 
     return out, kept_per_head, mask
 
 
+@_on_stream
 def solattn_forward_ex(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, Bq: int, Bk: int, mode="keep_correct",
                        rule="running_max", tau: float = 0.0, beta: float = 0.0, n_sink: int = 0,
                        correction="block", out: torch.Tensor | None = None,
@@ -357,6 +387,7 @@ def solattn_get_status(workspace: torch.Tensor, stream=None) -> int:
         return int(_lib.solattn_get_status(workspace.data_ptr(), _stream(stream, workspace.device)))
 
 
+@_on_stream
 def solattn_forward_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, Bq: int, Bk: int, tau: float,
                          mode="keep_correct", out: torch.Tensor | None = None,
                          kept_per_head: torch.Tensor | None = None, scratch: torch.Tensor | None = None,
@@ -388,6 +419,7 @@ def solattn_forward_host(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, Bq: 
     return out, kept_per_head
 
 
+@_on_stream
 def solattn_watchdog_selftest(limit_ns: int = 2_000_000, stream=None) -> int:
     """Run the device watchdog self-test; returns the status the kernel stored
     (SOLATTN_ETIMEOUT when a wait that nobody completes is abandoned on time)."""
@@ -401,6 +433,7 @@ def solattn_watchdog_selftest(limit_ns: int = 2_000_000, stream=None) -> int:
 NOALLOC_SCRATCH_BYTES = 64 << 20
 
 
+@_on_stream
 def solattn_forward_noalloc(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, Bq: int, Bk: int, tau: float,
                             mode="keep_correct", out: torch.Tensor | None = None,
                             kept_per_head: torch.Tensor | None = None, stream=None):
@@ -439,6 +472,7 @@ def _route_args(qbar: torch.Tensor, kbar: torch.Tensor, N: int, Bq: int, Bk: int
     return B, H, d, keep_mask
 
 
+@_on_stream
 def solattn_route_keep(qbar: torch.Tensor, kbar: torch.Tensor, N: int, Bq: int, Bk: int, tau: float,
                        keep_mask: torch.Tensor | None = None, stream=None) -> torch.Tensor:
     """The running-maximum routing rule alone on pooled blocks (fp32 [B, H, nB, d]); returns the
@@ -464,6 +498,7 @@ def _proxy_map(B, H, N, Bq, Bk, proxy_map, device):
     return proxy_map
 
 
+@_on_stream
 def solattn_route_topk(qbar: torch.Tensor, kbar: torch.Tensor, N: int, Bq: int, Bk: int, k: int,
                        keep_mask: torch.Tensor | None = None, proxy_map: torch.Tensor | None = None, stream=None):
     """Top-k routing (materialised proxy map, the k largest proxies per query block).
@@ -478,6 +513,7 @@ def solattn_route_topk(qbar: torch.Tensor, kbar: torch.Tensor, N: int, Bq: int, 
     return keep_mask, proxy_map
 
 
+@_on_stream
 def solattn_route_topp(qbar: torch.Tensor, kbar: torch.Tensor, N: int, Bq: int, Bk: int, p: float,
                        keep_mask: torch.Tensor | None = None, proxy_map: torch.Tensor | None = None, stream=None):
     """Top-p routing (materialised proxy map; the heaviest blocks until their share of the
@@ -492,6 +528,7 @@ def solattn_route_topp(qbar: torch.Tensor, kbar: torch.Tensor, N: int, Bq: int, 
     return keep_mask, proxy_map
 
 
+@_on_stream
 def solattn_selftest_exp2(x: torch.Tensor, stream=None) -> torch.Tensor:
     """2^x by the software exp2 of the softmax, for a contiguous fp32 CUDA tensor."""
     if x.dtype != torch.float32 or not x.is_cuda or not x.is_contiguous():
@@ -613,6 +650,11 @@ def solattn_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_len: to
             if rc:
                 _check(rc, "solattn_cross")
             return out
+    return _cross(q, k, v, key_len, out, workspace, stream)
+
+
+@_on_stream
+def _cross(q, k, v, key_len, out, workspace, stream):
     dt = DTYPES.get(getattr(q, "dtype", None))
     if dt is None or not q.is_cuda or q.dim() != 4:
         raise ValueError("q must be a bfloat16 or float16 [B, H, N, d] CUDA tensor")
@@ -707,6 +749,11 @@ def solattn_paged_forward(q: torch.Tensor, cache: PagedCache, table: torch.Tenso
             if rc:
                 _check(rc, "solattn_paged_forward")
             return out
+    return _paged(q, cache, table, cu, length, max_new, causal, out, workspace, stream)
+
+
+@_on_stream
+def _paged(q, cache, table, cu, length, max_new, causal, out, workspace, stream):
     dtype, total = cache._rows_dtype(q, "q")
     dev, H = cache.device, q.shape[1]
     shape = (total, H, cache.d)
@@ -734,6 +781,11 @@ def solattn_cache_append(cache: PagedCache, new_k: torch.Tensor, new_v: torch.Te
             if rc:
                 _check(rc, "solattn_cache_append")
             return
+    _append(cache, new_k, new_v, table, cu, length, workspace, stream)
+
+
+@_on_stream
+def _append(cache, new_k, new_v, table, cu, length, workspace, stream):
     dtype, total = cache._rows_dtype(new_k, "new_k")
     dev, shape = cache.device, (total, cache.Hkv, cache.d)
     seqs = cache._seqs(table, cu, length, total)
@@ -753,6 +805,11 @@ def solattn_cache_read(cache: PagedCache, table: torch.Tensor, cu: torch.Tensor,
             if rc:
                 _check(rc, "solattn_cache_read")
             return k_out, v_out
+    return _read(cache, table, cu, length, k_out, v_out, workspace, stream)
+
+
+@_on_stream
+def _read(cache, table, cu, length, k_out, v_out, workspace, stream):
     dtype, total = cache._rows_dtype(k_out, "k_out")
     dev, shape = cache.device, (total, cache.Hkv, cache.d)
     seqs = cache._seqs(table, cu, length, total)
