@@ -431,8 +431,12 @@ __device__ __forceinline__ void exp2_poly_x2(float x0, float x1, float &y0, floa
   y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
 }
 
-// The same, except that a NaN gives the largest finite number (fmin and fmax would drop it): the
-// clamps hand it through, and the integer sum below turns its bits into 0x7f7fffff.
+// The same, except that
+//   * 2^-125 and below is 0 (the clamp's value is subtracted: results from 2^-110 up differ by less than
+//     2^-15 of themselves, from 2^-100 up by nothing), so that a score of -infinity has no weight: 2^-125 is a
+//     normal number, and against values of 2^127, or where nothing else has weight, it would show;
+//   * a NaN gives the largest finite number (fmin and fmax would drop it): the clamps hand it through, and the
+//     integer sum below turns its bits into 0x7f7fffff.
 __device__ __forceinline__ void exp2_poly_nan_x2(float x0, float x1, float &y0, float &y1) {
   constexpr float kShift = 12582912.0f;  // 1.5 * 2^23
   constexpr float c0 = 0.9999280571937561f, c1 = 0.6932609677314758f;
@@ -450,8 +454,11 @@ __device__ __forceinline__ void exp2_poly_nan_x2(float x0, float x1, float &y0, 
   float p0, p1, t0, t1;
   f2_split(pp, p0, p1);
   f2_split(t, t0, t1);
-  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
-  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
+  constexpr float least = -c0 * 0x1p-125f;
+  f2_split(add2(f2(__int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23)),
+                   __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23))),
+                f2(least, least)),
+           y0, y1);
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

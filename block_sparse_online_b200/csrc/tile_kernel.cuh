@@ -743,11 +743,13 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
           if (m_ref != -CUDART_INF_F) alpha = ex2_approx(m_ref - mx);
           m_ref = mx;
         }
+        const float ms = m_ref == -CUDART_INF_F ? 0.f : m_ref;
         uint64_t acc[2] = {f2(0.f, 0.f), f2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 2; ++c)
-          exp_chunk(c, m_ref == -CUDART_INF_F ? 0.f : -m_ref, acc, std::true_type{});
-        lsum = total(acc);
+          exp_chunk(c, -ms, acc, std::true_type{});
+        // A maximum of +infinity or NaN makes the row NaN whatever the polynomial made of infinity - infinity.
+        lsum = total(acc) + (ms - ms);
       }
       l = l * alpha + lsum;
       if constexpr (C::BITS8) {

@@ -1,0 +1,123 @@
+"""Masks, infinities and magnitudes at which the dense attention's kernels could differ from the definition,
+in the rows kernel and in the tile kernel: each test names the kernel that it means and checks that it ran.
+Tolerances: tests/dense_util.py derives them."""
+import pytest
+import torch
+
+from block_sparse_online_b200 import solattn
+from tests import dense_util as du
+
+pytestmark = pytest.mark.gpu
+BF, FP = torch.bfloat16, torch.float16
+I8, E4 = torch.int8, torch.float8_e4m3fn
+KINDS = [(BF, None), (FP, None), (BF, I8), (FP, E4)]
+KIND_IDS = ["bf16", "fp16", "bf16-int8", "fp16-e4m3"]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+
+
+def gen(seed):
+    return torch.Generator(device="cuda").manual_seed(seed)
+
+
+def rnd(g, *shape, mul=1.0, dtype=BF):
+    return (torch.randn(*shape, generator=g, device="cuda") * mul).to(dtype)
+
+
+def run_on(kernel, call):
+    """call(), which has to launch `kernel` ("rows" or "tile") and not the other."""
+    with torch.profiler.profile(activities=[torch.profiler.ProfilerActivity.CUDA]) as p:
+        result = call()
+        torch.cuda.synchronize()
+    names = " ".join(e.key for e in p.key_averages())
+    ran = {k for k in ("rows", "tile") if f"{k}_kernel" in names}
+    assert ran == {kernel}, (ran, names)
+    return result
+
+
+# ------------------------------------------------------------------ columns without weight
+
+
+@pytest.mark.parametrize("kernel,n", [("rows", 15), ("tile", 1000)])
+@pytest.mark.parametrize("dtype,kind", KINDS, ids=KIND_IDS)
+def test_causal_rows_in_front_of_the_sequence_are_zero(kernel, n, dtype, kind):
+    """More new tokens than the sequence has keys: reported, and the tokens without a key are zeros."""
+    g, H, d, page = gen(1), 16, 128, 16
+    ns, lens = [n, n], [10, n]
+    k, v, ks, vs, table = du.make_cache(g, lens, H, page, d, dtype, kind)
+    q = rnd(g, 2 * n, H, d, dtype=dtype)
+    cache = solattn.PagedCache(k, v, ks, vs)
+    ws = solattn.alloc_paged_workspace(cache, 2, H, 2 * n)
+    out = run_on(kernel, lambda: solattn.solattn_paged_forward(q, cache, table, du.cu_of(ns), du.ints(lens), max_new=n,
+                                                               causal=True, workspace=ws))
+    assert solattn.solattn_get_status(ws) == solattn.SOLATTN_ETABLE
+    assert (out[:n - 10] == 0).all()
+    want, bound = du.paged_oracle(q, k, v, ks, vs, table, ns, lens, True, dtype)
+    du.check(out, want, bound)
+
+
+def cross_inputs(seed, n, Nk, dtype, d=64):
+    """q, k, v of 16 heads; element 0 of every query is 1 and of every key 0."""
+    g = gen(seed)
+    q, k, v = (rnd(g, 1, 16, m, d, dtype=dtype) for m in (n, Nk, Nk))
+    q[..., 0], k[..., 0] = 1.0, 0.0
+    return q, k, v
+
+
+@pytest.mark.parametrize("kernel,n", [("rows", 5), ("tile", 2000)])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+@pytest.mark.parametrize("Nk", [50, 300])
+def test_scores_of_minus_infinity(kernel, n, dtype, Nk):
+    """A row whose scores are all -inf is zero; with one finite score it is that key's value."""
+    q, k, v = cross_inputs(2, n, Nk, dtype)
+    k[..., 0] = -float("inf")
+    out = run_on(kernel, lambda: solattn.solattn_cross(q, k, v))
+    assert (out == 0).all()
+    for at in (0, Nk - 1):
+        kk = k.clone()
+        kk[:, :, at, 0] = 0.0
+        out = solattn.solattn_cross(q, kk, v)
+        # weight 1 and a sum of 1: the value itself, after the last rounding of it and of P
+        want = v[:, :, at:at + 1].expand_as(out).double()
+        du.check(out, want, want.abs() * (du.EPS[dtype] + 1.5e-4))
+
+
+@pytest.mark.parametrize("kernel,n", [("rows", 5), ("tile", 2000)])
+@pytest.mark.parametrize("at", [0, 5, 6, 7, 14, 15, 62, 63, 64, 70, 79, 127, 130, 134])
+def test_a_score_of_infinity_makes_the_row_nan(kernel, n, at):
+    q, k, v = cross_inputs(3, n, 300, BF)
+    k[:, :, at, 0] = float("inf")
+    assert run_on(kernel, lambda: solattn.solattn_cross(q, k, v)).isnan().all()
+
+
+@pytest.mark.parametrize("kernel,n", [("rows", 5), ("tile", 2000)])
+@pytest.mark.parametrize("score", [-8192.0, -1200.0, -float("inf")])
+def test_huge_values_of_keys_without_weight(kernel, n, score):
+    """A key hundreds of powers of two below the others has no weight, however large its value: 2^(1.44 score / 8)
+    times 2^127 is below 2^-88."""
+    for at in (14, 71, 128 + 6, 299):  # in a row's first step, in later ones, in the ragged last one
+        q, k, v = cross_inputs(4, n, 300, BF)
+        k[:, :, at, 0] = score
+        v[:, :, at] = 2.0 ** 127
+        out = run_on(kernel, lambda: solattn.solattn_cross(q, k, v))
+        if score == -float("inf"):
+            k[:, :, at, 0] = -8192.0
+        want, bound = du.cross_oracle(q, k, v, None, BF)
+        du.check(out, want, bound)
+
+
+@pytest.mark.parametrize("kernel,n", [("rows", 12), ("tile", 1000)])
+def test_huge_values_of_later_keys(kernel, n):
+    """Causal: a token's row does not see the large value of a token behind it."""
+    g, H, d, page = gen(5), 16, 64, 16
+    k, v, _, _, table = du.make_cache(g, [n], H, page, d, BF, None)
+    v[int(table[0, 0]), :, 7] = 2.0 ** 120
+    q = rnd(g, n, H, d, mul=0.5)
+    cache = solattn.PagedCache(k, v)
+    out = run_on(kernel, lambda: solattn.solattn_paged_forward(q, cache, table, du.cu_of([n]), du.ints([n]), max_new=n))
+    want, bound = du.paged_oracle(q, k, v, None, None, table, [n], [n], True, BF)
+    du.check(out, want, bound)
