@@ -329,8 +329,9 @@ __global__ void __launch_bounds__(kRowsWarps * 32, rows_blocks(NT)) rows_kernel(
         }
       }
       if constexpr (KIND != kKind16) {
-        if (__any_sync(0xffffffffu, fmaxf(vs0, vs1) > vref)) {
-          float mx = fmaxf(vs0, vs1);
+        const float vmag = fmaxf(fabsf(vs0), fabsf(vs1));  // (a scale may be negative)
+        if (__any_sync(0xffffffffu, vmag > vref)) {
+          float mx = vmag;
 #pragma unroll
           for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
           // the power of two above mx, from 2^-100 up (and down to 2^100: larger scales, and

@@ -466,7 +466,7 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
       int sl = kv % C::NSLOT;
       if (!wait(&sc.empty[sl], ((kv / C::NSLOT) & 1) ^ 1)) break;
       // scales: the reference is a power of two >= the largest value scale so far (2^-100 .. 2^100)
-      float mx = vsc;
+      float mx = fabsf(vsc);  // (a scale may be negative)
 #pragma unroll
       for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
       if (lane == 0) {

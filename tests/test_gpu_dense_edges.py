@@ -121,3 +121,25 @@ def test_huge_values_of_later_keys(kernel, n):
     out = run_on(kernel, lambda: solattn.solattn_paged_forward(q, cache, table, du.cu_of([n]), du.ints([n]), max_new=n))
     want, bound = du.paged_oracle(q, k, v, None, None, table, [n], [n], True, BF)
     du.check(out, want, bound)
+
+
+# ------------------------------------------------------------------ scales of 8-bit rows
+
+
+@pytest.mark.parametrize("kernel,n", [("rows", 3), ("tile", 1000)])
+@pytest.mark.parametrize("kind", [I8, E4], ids=["int8", "e4m3"])
+@pytest.mark.parametrize("which", ["all", "mixed", "mixed_large"])
+def test_negative_scales(kernel, n, kind, which):
+    """x = code * scale whatever the scale's sign, for keys and for values."""
+    g, H, d, page, L = gen(6), 8, 128, 32, 1300
+    k, v, ks, vs, table = du.make_cache(g, [L], H, page, d, BF, kind)
+    for s in (ks, vs):
+        sign = -1.0 if which == "all" else torch.where(torch.rand(s.shape, generator=g, device="cuda") < 0.5, -1.0, 1.0)
+        s.mul_(sign)
+        if which == "mixed_large":  # the negative ones far above the others
+            s.mul_(torch.where(s < 0, 2.0 ** (12 if s is vs else 1), 1.0))
+    q = rnd(g, n, H, d)
+    cache = solattn.PagedCache(k, v, ks, vs)
+    out = run_on(kernel, lambda: solattn.solattn_paged_forward(q, cache, table, du.cu_of([n]), du.ints([L]), max_new=n))
+    want, bound = du.paged_oracle(q, k, v, ks, vs, table, [n], [L], True, BF)
+    du.check(out, want, bound)
