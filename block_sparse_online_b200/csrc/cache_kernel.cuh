@@ -36,7 +36,7 @@ struct CacheArgs {
   void *new_k, *new_v;                                   // 16-bit rows: read (write call) or written (read call)
   long long nk_tok, nk_head, nv_tok, nv_head;
   const int *table, *cu, *len;
-  int width, page, page_shift, num_pages, B, Hkv, total, token_shift;
+  int width, page, page_shift, num_pages, B, Hkv, n, total, Lmax, token_shift;  // n: of calls without cu (there are none)
   int *status;
 };
 
@@ -98,13 +98,15 @@ __global__ void __launch_bounds__(kCacheThreads) cache_kernel(const __grid_const
   if constexpr (WRITE) load_rows(0);
   const bool in_smem = a.B < kCacheCu;
   if (in_smem) {
-    for (int i = threadIdx.x; i <= a.B; i += kCacheThreads) s_cu[i] = __ldg(a.cu + i);
+    for (int i = threadIdx.x; i <= a.B; i += kCacheThreads) s_cu[i] = first_row(a, __ldg(a.cu + i));
     __syncthreads();
   }
+  if (blockIdx.x == 0 && threadIdx.x >= kCacheThreads - 32) check_lengths(a);
   if (static_cast<int>(threadIdx.x) < nt) {
     const int tt = t0 + threadIdx.x;
-    auto cu = [&](int i) { return in_smem ? s_cu[i] : __ldg(a.cu + i); };
-    // last sequence that begins at or before the token: cu is ascending
+    auto cu = [&](int i) { return in_smem ? s_cu[i] : first_row(a, __ldg(a.cu + i)); };
+    // last sequence that begins at or before the token: cu is ascending (where it is not, a sequence that holds
+    // the token, or none)
     int lo = 0, hi = a.B;
     while (hi - lo > 1) {
       const int mid = (lo + hi) >> 1;
@@ -114,8 +116,8 @@ __global__ void __launch_bounds__(kCacheThreads) cache_kernel(const __grid_const
     const int end = cu(lo + 1);
     int page = -1, row = 0;
     if (tt >= cu(lo) && tt < end) {  // rows in front of the first and behind the last sequence are left alone
-      const int pos = __ldg(a.len + lo) - (end - tt);
-      bool ok = pos >= 0 && (pos >> a.page_shift) < a.width;
+      const int pos = keys_of(a, lo) - (end - tt);
+      bool ok = pos >= 0;  // and below Lmax, as the length is
       if (ok) {
         page = __ldg(a.table + static_cast<size_t>(lo) * a.width + (pos >> a.page_shift));
         ok = static_cast<unsigned>(page) < static_cast<unsigned>(a.num_pages);

@@ -326,7 +326,7 @@ int cache_impl(const solattn_cache *cache, const solattn_view *nk, const solattn
   a.nk_tok = nk->stride_n, a.nk_head = nk->stride_h, a.nv_tok = nv->stride_n, a.nv_head = nv->stride_h;
   a.table = s->table, a.cu = s->cu, a.len = s->len;
   a.width = s->width, a.page = cache->page, a.page_shift = page_shift(cache->page), a.num_pages = cache->num_pages;
-  a.B = s->B, a.Hkv = cache->Hkv, a.total = s->total;
+  a.B = s->B, a.Hkv = cache->Hkv, a.total = s->total, a.Lmax = s->width * cache->page;
   a.status = reinterpret_cast<int *>(static_cast<uint8_t *>(status) + 4);
   // Tokens of a block: the power of two that leaves two blocks per SM, at most its rows at a time (1560 tokens of
   // 12 heads written and read: 14.5 us with two, 18.6 with four or one, 20.9 with eight).

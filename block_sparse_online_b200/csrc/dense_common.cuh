@@ -62,19 +62,27 @@ struct Seq {
 };
 
 // Query tokens, keys and first query row of sequence b. Values outside the call's buffers
-// are cut to them, so that no access depends on unchecked device data.
-__device__ __forceinline__ Seq seq_of(const DenseArgs &a, int b) {
+// are cut to them, so that no access depends on unchecked device data. The cache calls (CacheArgs)
+// cut them the same way: what a call writes is what the attention over it assumes.
+template <class A>
+__device__ __forceinline__ int first_row(const A &a, int cu) { return min(max(cu, 0), a.total); }
+template <class A>
+__device__ __forceinline__ int keys_of(const A &a, int b) {
+  return a.len ? min(max(__ldg(a.len + b), 0), a.Lmax) : a.Lmax;
+}
+template <class A>
+__device__ __forceinline__ Seq seq_of(const A &a, int b) {
   Seq s;
   if (a.cu) {
-    const int lo = min(max(__ldg(a.cu + b), 0), a.total);
-    const int hi = min(max(__ldg(a.cu + b + 1), lo), a.total);
+    const int lo = first_row(a, __ldg(a.cu + b));
+    const int hi = max(first_row(a, __ldg(a.cu + b + 1)), lo);
     s.tok0 = lo;
     s.n = hi - lo;
   } else {
     s.tok0 = 0;
     s.n = a.n;
   }
-  s.L = a.len ? min(max(__ldg(a.len + b), 0), a.Lmax) : a.Lmax;
+  s.L = keys_of(a, b);
   return s;
 }
 
@@ -279,8 +287,9 @@ __device__ __forceinline__ int page_of(const DenseArgs &a, int b, int j) {
   return -1;
 }
 
-// Lengths that seq_of had to cut are recorded once per call, by the first warp of block 0.
-__device__ __forceinline__ void check_lengths(const DenseArgs &a) {
+// Lengths that seq_of had to cut are recorded once per call, by one warp of block 0.
+template <class A>
+__device__ __forceinline__ void check_lengths(const A &a) {
   for (int b = threadIdx.x & 31; b < a.B; b += 32) {
     bool bad = false;
     if (a.cu) bad = a.cu[b] < 0 || a.cu[b + 1] < a.cu[b] || a.cu[b + 1] > a.total;

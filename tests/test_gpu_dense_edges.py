@@ -143,3 +143,71 @@ def test_negative_scales(kernel, n, kind, which):
     out = run_on(kernel, lambda: solattn.solattn_paged_forward(q, cache, table, du.cu_of([n]), du.ints([L]), max_new=n))
     want, bound = du.paged_oracle(q, k, v, ks, vs, table, [n], [L], True, BF)
     du.check(out, want, bound)
+
+
+# ------------------------------------------------------------------ lengths out of range, written and read
+
+
+@pytest.mark.parametrize("kind", [None, I8], ids=["16", "int8"])
+@pytest.mark.parametrize("cu,lens,total", [
+    ([0, 12], [64], 10),               # behind the packed rows: cut to 10 tokens, positions 54 .. 63
+    ([0, 4, 1 << 30], [20, 64], 10),
+    ([-5, 3, 10], [40, 64], 10),       # in front of them: cut to [0, 3)
+    ([0, 7, 4, 4], [64, 30, 33], 10),  # descending: the second and third sequence are empty
+    ([0, 5, 10], [1 << 30, 65], 10),   # longer than the table
+    ([0, 5, 10], [-1, 64], 10),        # no keys at all: nothing is written
+    ([0, 10], [3], 10),                # more new tokens than keys: those in front of the sequence are dropped
+], ids=str)
+def test_cache_lengths_are_cut_as_the_attention_cuts_them(cu, lens, total, kind):
+    """What append writes is where the attention looks for it, what cannot be written is left alone, and either
+    call reports it."""
+    g, Hkv, d, page = gen(7), 2, 64, 16
+    B, width = len(lens), 4
+    pages = [torch.randn(B * width, Hkv, page, d, generator=g, device="cuda") for _ in range(2)]
+    if kind is None:
+        k, v, ks, vs = pages[0].to(BF), pages[1].to(BF), None, None
+    else:
+        k, v = ((x * 20).to(kind) for x in pages)
+        ks, vs = (torch.rand(B * width, Hkv, page, generator=g, device="cuda") for _ in range(2))
+    cache = solattn.PagedCache(k, v, ks, vs)
+    table = torch.randperm(B * width, generator=g, device="cuda").to(torch.int32).reshape(B, width)
+    new = rnd(g, total, Hkv, d), rnd(g, total, Hkv, d)
+    want = [x.clone() for x in (k, v)], [None if x is None else x.clone() for x in (ks, vs)]
+    rows = {}
+    for b in range(B):  # as the attention cuts them
+        lo = min(max(cu[b], 0), total)
+        hi = max(min(max(cu[b + 1], 0), total), lo)
+        L = min(max(lens[b], 0), width * page)
+        for i in range(lo, hi):
+            if L - (hi - i) >= 0:
+                rows[i] = (int(table[b, (L - (hi - i)) // page]), (L - (hi - i)) % page)
+    for i, (at, r) in rows.items():
+        for w in range(2):
+            if kind is None:
+                want[0][w][at, :, r] = new[w][i]
+            else:
+                codes, sc = du.quantise(new[w][i], kind)
+                want[0][w][at, :, r] = codes.to(kind)
+                want[1][w][at, :, r] = sc
+    st = solattn.alloc_status()
+    args = table, du.ints(cu), du.ints(lens)
+    solattn.solattn_cache_append(cache, *new, *args, workspace=st)
+    assert solattn.solattn_get_status(st) == solattn.SOLATTN_ETABLE
+    for got, x in zip((k, v), want[0]):
+        assert torch.equal(got, x)
+    if kind is not None:
+        for got, x in zip((ks, vs), want[1]):
+            assert torch.equal(got, x)
+    out = torch.full_like(new[0], 7.0), torch.full_like(new[1], 7.0)
+    st = solattn.alloc_status()
+    solattn.solattn_cache_read(cache, *args, *out, workspace=st)
+    assert solattn.solattn_get_status(st) == solattn.SOLATTN_ETABLE
+    for w in range(2):
+        for i in range(total):
+            if i in rows:
+                at, r = rows[i]
+                x = want[0][w][at, :, r]
+                x = x if kind is None else (x.float() * want[1][w][at, :, r][..., None]).to(BF)
+                assert torch.equal(out[w][i], x)
+            else:
+                assert (out[w][i] == 7).all()
