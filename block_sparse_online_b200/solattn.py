@@ -586,14 +586,15 @@ def _int32(x, name, numel, device):
     return x.data_ptr()
 
 
-def _workspace(workspace, need, device):
-    """The caller's workspace (the library checks its size), or a new one with its header cleared."""
+def _workspace(workspace, need, device, least=0):
+    """The caller's workspace of at least ``least`` bytes (of a workspace proper the library checks the size, a status
+    word alone it takes by its address), or a new one with its header cleared."""
     if workspace is None:
         workspace = torch.empty(need(), dtype=torch.uint8, device=device)
         workspace[:256].zero_()
     elif not (isinstance(workspace, _Tensor) and workspace.dtype is _u8 and workspace.get_device() == device.index
-              and workspace.is_contiguous()):
-        _check_buffer(workspace, "workspace", (torch.uint8, torch.int8), 0, device)
+              and workspace.is_contiguous() and workspace.numel() >= least):
+        _check_buffer(workspace, "workspace", (torch.uint8, torch.int8), least, device)
     return workspace
 
 
@@ -789,7 +790,7 @@ def _append(cache, new_k, new_v, table, cu, length, workspace, stream):
     dtype, total = cache._rows_dtype(new_k, "new_k")
     dev, shape = cache.device, (total, cache.Hkv, cache.d)
     seqs = cache._seqs(table, cu, length, total)
-    workspace = _workspace(workspace, lambda: 256, dev)
+    workspace = _workspace(workspace, lambda: 256, dev, 256)
     rc = _on_device(dev, stream, _lib.solattn_cache_append, cache._c, _view3(new_k, "new_k", dtype, shape, dev),
                     _view3(new_v, "new_v", dtype, shape, dev), seqs, DTYPES[dtype], workspace.data_ptr())
     _check(rc, "solattn_cache_append")
@@ -813,7 +814,7 @@ def _read(cache, table, cu, length, k_out, v_out, workspace, stream):
     dtype, total = cache._rows_dtype(k_out, "k_out")
     dev, shape = cache.device, (total, cache.Hkv, cache.d)
     seqs = cache._seqs(table, cu, length, total)
-    workspace = _workspace(workspace, lambda: 256, dev)
+    workspace = _workspace(workspace, lambda: 256, dev, 256)
     rc = _on_device(dev, stream, _lib.solattn_cache_read, cache._c, seqs, _view3(k_out, "k_out", dtype, shape, dev),
                     _view3(v_out, "v_out", dtype, shape, dev), DTYPES[dtype], workspace.data_ptr())
     _check(rc, "solattn_cache_read")
