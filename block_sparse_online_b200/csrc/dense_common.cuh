@@ -315,7 +315,7 @@ __device__ __forceinline__ void pdl_launch_dependents() { asm volatile("griddepc
 __device__ __forceinline__ void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 // Joins the parts of each split item: o = sum_i 2^(m_i - m) o_i / sum_i 2^(m_i - m) l_i with
-// m the largest m_i, in the order of the blocks that wrote them. Grid (P, row chunks): the
+// m the largest m_i (l_i times the root of its factor twice: see the rows kernel on 8-bit caches), in the order of the blocks that wrote them. Grid (P, row chunks): the
 // blocks of column c take the item that block c of the attention launch begins, if others
 // end it; most have none. Reads 4 (d + 2) bytes a row and part. Launched as a programmatic
 // dependent: it is resident when the attention ends, which saves the gap between launches.
@@ -340,8 +340,8 @@ __global__ void __launch_bounds__(256) join_kernel(const DenseArgs a) {
       const float ms = m == -CUDART_INF_F ? 0.f : m;
       for (int p = 0; p < parts; ++p) {
         const size_t sl = p == 0 ? 2 * c + 1 : 2 * (c + p);
-        const float w = ex2_approx(a.part_ml[sl * 512 + r] - ms);
-        l = fmaf(w, a.part_ml[sl * 512 + 256 + r], l);
+        const float root = ex2_approx(0.5f * (a.part_ml[sl * 512 + r] - ms)), w = root * root;
+        l = fmaf(root, root * a.part_ml[sl * 512 + 256 + r], l);
         const float4 x = *reinterpret_cast<const float4 *>(a.part_o + ((sl * 2 + (r >> 7)) * (D / 4) + e) * 512 + (r & 127) * 4);
         o0 = fmaf(w, x.x, o0);
         o1 = fmaf(w, x.y, o1);
@@ -383,11 +383,12 @@ __global__ void __launch_bounds__(256) join_kernel(const DenseArgs a) {
 #pragma unroll
       for (int off = 16; off; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
       const float mn = fmaxf(m, mx), ms = mn == -CUDART_INF_F ? 0.f : mn;
-      const float old = ex2_approx(m - ms), w = ex2_approx(mp - ms);  // (0 for -infinity)
-      lp *= w;
+      const float old_root = ex2_approx(0.5f * (m - ms)), root = ex2_approx(0.5f * (mp - ms));  // (0 for -infinity)
+      const float old = old_root * old_root, w = root * root;
+      lp = lp * root * root;
 #pragma unroll
       for (int off = 16; off; off >>= 1) lp += __shfl_xor_sync(0xffffffffu, lp, off);
-      l = fmaf(l, old, lp);
+      l = fmaf(l * old_root, old_root, lp);
 #pragma unroll
       for (int e = 0; e < CPL; ++e) o[e] *= old;
       m = mn;

@@ -442,8 +442,8 @@ __device__ __forceinline__ void exp2_poly_nan_x2(float x0, float x1, float &y0, 
   constexpr float c0 = 0.9999280571937561f, c1 = 0.6932609677314758f;
   constexpr float c2 = 0.2426111251115799f, c3 = 0.0551716685295105f;
   float a0, a1;
-  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(a0) : "f"(x0), "f"(-125.f), "f"(64.f));
-  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(a1) : "f"(x1), "f"(-125.f), "f"(64.f));
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(a0) : "f"(x0), "f"(-125.f), "f"(126.f));
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(a1) : "f"(x1), "f"(-125.f), "f"(126.f));
   const uint64_t x = f2(a0, a1);
   const uint64_t t = add2(x, f2(kShift, kShift));
   const uint64_t nf = add2(t, f2(-kShift, -kShift));

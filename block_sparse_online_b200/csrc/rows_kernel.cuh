@@ -21,11 +21,15 @@
 // error as the output's own rounding. Maxima, sums and O stay in 32 bits.
 //
 // 8-bit caches: codes are expanded to fp16 (exact: int8 has 8 bits, e4m3 four and a range
-// that fp16 holds). A key's scale multiplies its score in 32 bits. A value's scale
-// multiplies its probability before that is rounded, divided by a power of two >= the
-// largest value scale met so far (exact; O follows when it grows), so the product stays in
-// fp16's range for caches of any magnitude. Queries in bf16 become fp16 after a division of each row
-// by a power of two that brings its largest element to [2^14, 2^15): exact down to 2^-31 of that element.
+// that fp16 holds). A key's scale multiplies its score in 32 bits. A value's scale s_j multiplies its
+// probability before that is rounded, and the row's reference is the maximum of x_j + log2 |s_j| over the keys
+// that the row sees, not of the scores x_j: then the products 2^(x_j - m) s_j are at most 2^8 and the largest is at least 1,
+// for caches of any magnitude (2^-100 to 2^100) and scales of any spread, and a product is off by 2^-11 of itself or,
+// below 2^-14 of the largest, by at most 2^-25 of that. Keys that a row does not see, or that have
+// no weight, take no bits from the others. The sum of weights is kept in 32 bits in the same units, which reach from 2^-100 to
+// 2^100: where the reference moves by more than a factor holds, the sum takes the factor's root twice.
+// Queries in bf16 become fp16 after a division of each row by a power of two that brings its largest element to
+// [2^14, 2^15): exact down to 2^-31 of that element.
 //
 // Bound by memory: at 32 sequences of 1 to 16384 keys, 4 key heads of 128, bf16, one token each, it reads
 // 551 MB in 85.5 us (6.4 TB/s). In e4m3 at 118800 keys of 24 heads (753 MB) it takes 141 us (5.3 TB/s): half the
@@ -102,6 +106,9 @@ template <int KIND>
 __device__ __forceinline__ uint32_t code_word(uint32_t x) {
   return KIND == kKindInt8 ? x ^ 0x80808080u : x;
 }
+
+// log2 of a value scale's magnitude, for the reference of a row: cut to +-100, which a scale of 0, and one beyond, takes.
+__device__ __forceinline__ float log2_scale(float x) { return fminf(fmaxf(__log2f(fabsf(x)), -100.f), 100.f); }
 
 constexpr int kRowsWarps = 4;
 constexpr float kRowsSlack = 8.0f;  // log2 units the reference maximum may lag
@@ -197,8 +204,6 @@ __global__ void __launch_bounds__(kRowsWarps * 32, rows_blocks(NT)) rows_kernel(
 #pragma unroll
       for (int i = 0; i < C::KS; ++i) o[nt][i][0] = o[nt][i][1] = o[nt][i][2] = o[nt][i][3] = 0.f;
     }
-    float vref = 0.f, vinv = 1.f;  // reference of the value scales and its reciprocal
-
     const uint8_t *kbase = static_cast<const uint8_t *>(a.k) + h * a.k_head * ES;
     const uint8_t *vbase = static_cast<const uint8_t *>(a.v) + h * a.v_head * ES;
     // Page of a group of 16 keys (contiguous keys: the batch index); -1: not to be read.
@@ -301,52 +306,35 @@ __global__ void __launch_bounds__(kRowsWarps * 32, rows_blocks(NT)) rows_kernel(
           for (int e = 0; e < 4; ++e)
             if (gr0 * 16 + g + 8 * (e >> 1) >= lim[nt][e & 1]) sc[nt][e] = -CUDART_INF_F;
       }
+      float lv0 = 0.f, lv1 = 0.f;
+      if constexpr (KIND != kKind16) lv0 = log2_scale(vs0), lv1 = log2_scale(vs1);
+      auto top = [&](int nt, int e) { return fmaxf(sc[nt][e] + lv0, sc[nt][e + 2] + lv1); };
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-        for (int e = 0; e < 2; ++e) grow |= fmaxf(sc[nt][e], sc[nt][e + 2]) > m[nt][e] + kRowsSlack;
+        for (int e = 0; e < 2; ++e) grow |= top(nt, e) > m[nt][e] + kRowsSlack;
       if (__any_sync(0xffffffffu, grow)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           float al[2];
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float mx = fmaxf(sc[nt][e], sc[nt][e + 2]);
+            float mx = top(nt, e);
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
             mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
             al[e] = 1.f;
             if (mx > m[nt][e] + kRowsSlack) {
-              if (m[nt][e] != -CUDART_INF_F) al[e] = ex2_approx(m[nt][e] - mx);
+              if (m[nt][e] != -CUDART_INF_F) al[e] = ex2_approx(0.5f * (m[nt][e] - mx));
               m[nt][e] = mx;
             }
-            l[nt][e] *= al[e];
+            l[nt][e] = l[nt][e] * al[e] * al[e];  // (the square may be below 2^-126 where l is above 2^100)
+            al[e] *= al[e];
           }
 #pragma unroll
           for (int i = 0; i < C::KS; ++i)
 #pragma unroll
             for (int e = 0; e < 4; ++e) o[nt][i][e] *= al[e & 1];
-        }
-      }
-      if constexpr (KIND != kKind16) {
-        const float vmag = fmaxf(fabsf(vs0), fabsf(vs1));  // (a scale may be negative)
-        if (__any_sync(0xffffffffu, vmag > vref)) {
-          float mx = vmag;
-#pragma unroll
-          for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-          // the power of two above mx, from 2^-100 up (and down to 2^100: larger scales, and
-          // infinite ones, overflow the result as they would in 32 bits)
-          const int ex = min(max((__float_as_int(mx) >> 23) + 1, 27), 227);
-          const float vnew = __int_as_float(ex << 23);
-          const float f = vref * __int_as_float((254 - ex) << 23);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int i = 0; i < C::KS; ++i)
-#pragma unroll
-              for (int e = 0; e < 4; ++e) o[nt][i][e] *= f;
-          vref = vnew;
-          vinv = __int_as_float((254 - ex) << 23);
         }
       }
       // ---- P^T, to the layout of the second product
@@ -358,10 +346,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, rows_blocks(NT)) rows_kernel(
         float p2 = ex2_approx(sc[nt][2] - m0), p3 = ex2_approx(sc[nt][3] - m1);
         l[nt][0] += p0 + p2;
         l[nt][1] += p1 + p3;
-        if constexpr (KIND != kKind16) {
-          const float f0 = vs0 * vinv, f1 = vs1 * vinv;
-          p0 *= f0, p1 *= f0, p2 *= f1, p3 *= f1;
-        }
+        if constexpr (KIND != kKind16) p0 *= vs0, p1 *= vs0, p2 *= vs1, p3 *= vs1;
         pb[nt][0] = transpose8(pack16<MT>(p0, p1));
         pb[nt][1] = transpose8(pack16<MT>(p2, p3));
       }
@@ -396,7 +381,6 @@ __global__ void __launch_bounds__(kRowsWarps * 32, rows_blocks(NT)) rows_kernel(
     }
 
     // ---- join the warps
-    const float vmul = KIND == kKind16 ? 1.f : vref;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
 #pragma unroll
@@ -415,10 +399,10 @@ __global__ void __launch_bounds__(kRowsWarps * 32, rows_blocks(NT)) rows_kernel(
         // columns of m tile i: 16-bit d = 128 pairs columns 64 apart, the others neighbours
         const int d0 = (KIND == kKind16 && D == 128) ? g * 8 + i : g * (D / 8) + 2 * i;
         const int d1 = (KIND == kKind16 && D == 128) ? d0 + 64 : d0 + 1;
-        sm.o[warp][nt * 8 + 2 * c][d0] = o[nt][i][0] * vmul;
-        sm.o[warp][nt * 8 + 2 * c + 1][d0] = o[nt][i][1] * vmul;
-        sm.o[warp][nt * 8 + 2 * c][d1] = o[nt][i][2] * vmul;
-        sm.o[warp][nt * 8 + 2 * c + 1][d1] = o[nt][i][3] * vmul;
+        sm.o[warp][nt * 8 + 2 * c][d0] = o[nt][i][0];
+        sm.o[warp][nt * 8 + 2 * c + 1][d0] = o[nt][i][1];
+        sm.o[warp][nt * 8 + 2 * c][d1] = o[nt][i][2];
+        sm.o[warp][nt * 8 + 2 * c + 1][d1] = o[nt][i][3];
       }
     }
     __syncthreads();
@@ -435,8 +419,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, rows_blocks(NT)) rows_kernel(
       float ll = 0.f, x0 = 0.f, x1 = 0.f, x2 = 0.f, x3 = 0.f;
 #pragma unroll
       for (int w = 0; w < kRowsWarps; ++w) {
-        const float f = ex2_approx(sm.m[w][r] - ms);
-        ll = fmaf(f, sm.l[w][r], ll);
+        const float root = ex2_approx(0.5f * (sm.m[w][r] - ms)), f = root * root;
+        ll = fmaf(root, root * sm.l[w][r], ll);
         const float4 y = *reinterpret_cast<const float4 *>(&sm.o[w][r][4 * e]);
         x0 = fmaf(f, y.x, x0);
         x1 = fmaf(f, y.y, x1);

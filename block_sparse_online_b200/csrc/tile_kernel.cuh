@@ -25,7 +25,9 @@
 // one) the maximum is taken (a NaN wins it) and the step done again. P is rounded to the 16-bit type of the
 // keys, fp16 for 8-bit caches: off by at most 2^-8 (bf16) or 2^-11 of each value, independently from key to
 // key, which adds about as much to the result's error as the output's own rounding. The reference, sums and
-// O are in 32 bits. Two pairs of exponentials in eight go through the polynomial on the FMA pipe.
+// O are in 32 bits. Two pairs of exponentials in eight go through the polynomial on the FMA pipe. 8-bit caches:
+// the reference is that of x + log2 |value scale|, as in the rows kernel; that no product of P and a scale is
+// large is shown by the row sum times the unit's largest scale.
 //
 // What bounds it, measured at 1560 tokens x 32760 keys x 12 heads of 128 in bf16 (350 to 400 us, 800 to 900
 // TFLOP/s; the card's power limit moves it): the tensor core's instructions. A step's 8 products of 64 columns
@@ -106,11 +108,11 @@ struct TileCtl {
   uint32_t turn;
   uint32_t tmem_base;
   int abort_flag;
-  float wmax[2][4];              // converter: largest value scale per warp
   alignas(16) float ks[C::BITS8 ? C::NSC : 1][C::BITS8 ? 128 : 4];  // key scales (x log2(e) / sqrt d)
-  alignas(16) float vs[C::BITS8 ? C::NSC : 1][C::BITS8 ? 128 : 4];  // value scales over the reference
-  float vgrow[C::NSC], vref[C::NSC];  // factor of O when the reference grew, and the reference
-  uint32_t qmax[4];              // converter: largest query of the tile per warp (bf16 bits)
+  alignas(16) float vs[C::BITS8 ? C::NSC : 1][C::BITS8 ? 128 : 4];  // value scales
+  alignas(16) float lv[C::BITS8 ? C::NSC : 1][C::BITS8 ? 128 : 4];  // their log2_scale()
+  alignas(16) float wmax[C::NSC][4];  // largest magnitude of the value scales, by the converter's warps
+  uint32_t qmax[2][4];           // converter: largest query of a tile per warp (bf16 bits); tiles alternate
 };
 
 template <class C>
@@ -312,7 +314,7 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
   const volatile int *ab = &sc.abort_flag;
   const int tid = threadIdx.x & 127, warp = tid >> 5, lane = tid & 31;
   const int rl = tid / LPR, pc = tid % LPR;
-  uint32_t kv = 0, qi = 0, tile = 0, conv_ph = 0;
+  uint32_t kv = 0, qi = 0, tile = 0, item = 0;
   bool ok = true;
   auto wait = [&](uint64_t *bar, uint32_t par) {
     bool w = mbar_sleep(bar, par, a.timeout_ns, ab);
@@ -418,12 +420,12 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
       }
       big = __reduce_max_sync(0xffffffffu, big);
       if (lane == 0) {
-        sc.qmax[warp] = big;
+        sc.qmax[item & 1][warp] = big;
         mbar_arrive(&sc.conv);
       }
-      if (!wait(&sc.conv, conv_ph)) break;
-      conv_ph ^= 1;
-      big = max(max(sc.qmax[0], sc.qmax[1]), max(sc.qmax[2], sc.qmax[3]));
+      if (!wait(&sc.conv, item & 1)) break;
+      big = max(max(sc.qmax[item & 1][0], sc.qmax[item & 1][1]), max(sc.qmax[item & 1][2], sc.qmax[item & 1][3]));
+      ++item;
       const int ex = static_cast<int>(big >> 7);  // biased exponent
       const int sh = ex == 0 ? 0 : min(max(141 - ex, -126), 126);
       up = __int_as_float((127 + sh) << 23);
@@ -450,7 +452,6 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
     if (!ok) break;
     const float kmul = a.scale_log2 * down;
     // ---- units: K u, then V u, each with the next piece's codes on their way
-    float vref = 0.f;
     const Segment *nxt = nullptr;
     const int u1 = g->u0 + g->n;
     for (int u = g->u0; u < u1 && ok; ++u) {
@@ -465,28 +466,14 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
       const int entries = f ? fetch_entries(*f, fu) : -2;
       int sl = kv % C::NSLOT;
       if (!wait(&sc.empty[sl], ((kv / C::NSLOT) & 1) ^ 1)) break;
-      // scales: the reference is a power of two >= the largest value scale so far (2^-100 .. 2^100)
+      const int ss = tile % C::NSC;
       float mx = fabsf(vsc);  // (a scale may be negative)
 #pragma unroll
       for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, o));
-      if (lane == 0) {
-        sc.wmax[tile & 1][warp] = mx;
-        mbar_arrive(&sc.conv);
-      }
-      if (!wait(&sc.conv, conv_ph)) break;
-      conv_ph ^= 1;
-      mx = fmaxf(fmaxf(sc.wmax[tile & 1][0], sc.wmax[tile & 1][1]), fmaxf(sc.wmax[tile & 1][2], sc.wmax[tile & 1][3]));
-      float growth = 1.f;
-      if (mx > vref) {
-        const int ex = min(max((__float_as_int(mx) >> 23) + 1, 27), 227);
-        const float vnew = __int_as_float(ex << 23);
-        growth = vref * __int_as_float((254 - ex) << 23);
-        vref = vnew;
-      }
-      const int ss = tile % C::NSC;
+      if (lane == 0) sc.wmax[ss][warp] = mx;
       sc.ks[ss][tid] = ksc * kmul;
-      sc.vs[ss][tid] = vref > 0.f ? vsc * __int_as_float((254 << 23) - __float_as_int(vref)) : vsc;
-      if (tid == 0) sc.vgrow[ss] = growth, sc.vref[ss] = vref;
+      sc.vs[ss][tid] = vsc;
+      sc.lv[ss][tid] = log2_scale(vsc);
       ++tile;
       expand(ring + sl * C::HALF_BYTES, ck);
       publish(&sc.full[sl]);
@@ -647,7 +634,7 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
     const int lim = row_in(*sg) ? (a.causal ? min(max(sg->lim0 + my_tok, 0), sg->L) : sg->L) : sg->klim;
     const uint32_t qe = qi + w;
     qi += 2;
-    float m_ref = -CUDART_INF_F, l = 0.f, vref = 0.f;
+    float m_ref = -CUDART_INF_F, l = 0.f;
     for (int j = 0; j < ns; ++j) {
       const int b = j & 1;
       if (!wait(&sc.s_full[w][b], s_n[b] + (j >> 1))) break;
@@ -667,9 +654,10 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
       if (leader && b == 1 && j >= 3) release(kv + j - 2);
       const int base = sg->u0 * kUnitKeys + j * kStepKeys;
       const int left = lim - base;  // keys of this step that the row sees
-      float alpha = 1.f, lsum = 0.f;
+      float grow = 1.f, lsum = 0.f;  // root of the factor of O and l
       const float *kscale = C::BITS8 ? &sc.ks[(tile + (j >> 1)) % C::NSC][b * kStepKeys] : nullptr;
       const float *vscale = C::BITS8 ? &sc.vs[(tile + (j >> 1)) % C::NSC][b * kStepKeys] : nullptr;
+      const float *lscale = C::BITS8 ? &sc.lv[(tile + (j >> 1)) % C::NSC][b * kStepKeys] : nullptr;
       // P = 2^(x f - m) of 32-column chunk c; f: the logit scale, a key's own scale, or 1 (PRE: x is
       // scaled already).
       auto exp_chunk = [&](int c, float neg_m, uint64_t(&acc)[2], auto pre_tag) {
@@ -717,7 +705,12 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
 #pragma unroll
         for (int c = 0; c < 2; ++c) exp_chunk(c, -m_ref, acc, std::false_type{});
         lsum = total(acc);
-        return __all_sync(0xffffffffu, lsum <= kTileSumLimit);
+        float most = lsum;  // of the probabilities that were packed
+        if constexpr (C::BITS8) {
+          const float4 w = *reinterpret_cast<const float4 *>(sc.wmax[(tile + (j >> 1)) % C::NSC]);
+          most *= fmaxf(fmaxf(fmaxf(w.x, w.y), fmaxf(w.z, w.w)), 0x1p-85f);  // (and the sum itself is <= 2^100)
+        }
+        return __all_sync(0xffffffffu, most <= kTileSumLimit);
       };
       const bool plain = __all_sync(0xffffffffu, left >= kStepKeys);
       bool done = false;
@@ -737,10 +730,14 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
         }
         float mxs[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};
 #pragma unroll
-        for (int e = 0; e < kStepKeys; e += 2) mxs[(e >> 1) & 3] = fmax3_nan(mxs[(e >> 1) & 3], u2f_(x[e]), u2f_(x[e + 1]));
+        for (int e = 0; e < kStepKeys; e += 2) {
+          float z0 = u2f_(x[e]), z1 = u2f_(x[e + 1]);
+          if constexpr (C::BITS8) z0 += lscale[e], z1 += lscale[e + 1];
+          mxs[(e >> 1) & 3] = fmax3_nan(mxs[(e >> 1) & 3], z0, z1);
+        }
         const float mx = fmax3_nan(mxs[0], mxs[1], fmax3_nan(mxs[2], mxs[3], mxs[3]));
         if (!(mx <= m_ref + kTileSlack)) {
-          if (m_ref != -CUDART_INF_F) alpha = ex2_approx(m_ref - mx);
+          if (m_ref != -CUDART_INF_F) grow = ex2_approx(0.5f * (m_ref - mx));
           m_ref = mx;
         }
         const float ms = m_ref == -CUDART_INF_F ? 0.f : m_ref;
@@ -751,14 +748,9 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
         // A maximum of +infinity or NaN makes the row NaN whatever the polynomial made of infinity - infinity.
         lsum = total(acc) + (ms - ms);
       }
-      l = l * alpha + lsum;
-      if constexpr (C::BITS8) {
-        if (b == 0) {
-          alpha *= sc.vgrow[(tile + (j >> 1)) % C::NSC];
-          vref = sc.vref[(tile + (j >> 1)) % C::NSC];
-        }
-      }
-      if (j > 0 && __any_sync(0xffffffffu, alpha != 1.f)) {
+      l = l * grow * grow + lsum;  // (the square may be below 2^-126 where l is above 2^100)
+      if (j > 0 && __any_sync(0xffffffffu, grow != 1.f)) {
+        const float alpha = grow * grow;
         // O is at rest once P V of the step before has completed: its commit is that of S(j + 1), if there is one.
         if (!(j + 1 < ns ? wait(&sc.s_full[w][b ^ 1], s_n[b ^ 1] + ((j + 1) >> 1)) : wait(&sc.o_pre[w], pre_n))) break;
 #pragma unroll 1
@@ -804,7 +796,6 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
       for (int i = last >= 3 ? (last - 1) / 2 : 0; i < n; ++i) release(kv + 2 * i + 1);
     }
     kv += 2 * n;
-    const float vm = C::BITS8 ? vref : 1.f;
     if (sg->part >= 0) {
       // Partial result, [slot][half][column / 4][row][4]: a warp's stores are contiguous.
       const size_t slot = sg->part;
@@ -818,7 +809,7 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
 #pragma unroll
         for (int e = 0; e < 32; e += 4)
           *reinterpret_cast<float4 *>(dst + (c * 8 + e / 4) * (128 * 4)) =
-              make_float4(u2f_(o[e]) * vm, u2f_(o[e + 1]) * vm, u2f_(o[e + 2]) * vm, u2f_(o[e + 3]) * vm);
+              make_float4(u2f_(o[e]), u2f_(o[e + 1]), u2f_(o[e + 2]), u2f_(o[e + 3]));
       }
       a.part_ml[slot * 512 + w * 128 + row] = m_ref;
       a.part_ml[slot * 512 + 256 + w * 128 + row] = l;
@@ -828,7 +819,7 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
       // Complete rows: through this half's query buffer (every product with it is done), so that
       // a warp writes whole lines: its 32 rows one by one would touch 32 lines with every
       // store (measured: 3300 cycles a half, and the stores held up the barriers behind them).
-      const float inv = l == 0.f ? 0.f : vm / l;  // a row that sees no key is zero
+      const float inv = l == 0.f ? 0.f : 1.f / l;  // a row that sees no key is zero
       uint8_t *buf = q_smem + (qe % C::NQ) * C::HALF_BYTES;
 #pragma unroll
       for (int c = 0; c < D / 32; ++c) {

@@ -211,3 +211,121 @@ def test_cache_lengths_are_cut_as_the_attention_cuts_them(cu, lens, total, kind)
                 assert torch.equal(out[w][i], x)
             else:
                 assert (out[w][i] == 7).all()
+
+
+# ------------------------------------------------------------------ 8-bit rows whose scales differ
+
+
+def paged_oracle8(q, k, v, ks, vs, table, ns, lens, causal, dtype):
+    """As du.paged_oracle, with a bound that knows of the keys that a row SEES alone. P times the value's scale is rounded
+    to fp16 in units in which the row's largest such product is at least 1: a product below 2^-14 of that is off by at
+    most 2^-25, so the row by 2^-25 max_j (w_j |scale_j|) sum_j |code_j|, j over the keys that it sees."""
+    total, H, d = q.shape
+    Hkv, page = k.shape[1], k.shape[2]
+    G = H // Hkv
+    o = torch.zeros(total, H, d, dtype=torch.float64, device=q.device)
+    bound = torch.zeros_like(o)
+    t0 = 0
+    for b, (n, L) in enumerate(zip(ns, lens)):
+        kk, _, _ = du.cached(k, ks, table[b], page, L)
+        vv, codes, _ = du.cached(v, vs, table[b], page, L)
+        pos = torch.arange(L, device=q.device)
+        scale = vs[table[b].long()[pos // page], :, pos % page].double().abs().t()  # [Hkv, L]
+        i = torch.arange(n, device=q.device)
+        limit = L - n + i + 1 if causal else torch.full_like(i, L)
+        seen = pos[None, :] < limit[:, None]
+        for h in range(H):
+            x, g = q[t0:t0 + n, h].double(), h // G
+            o[t0:t0 + n, h], tight = du.attend(x, kk[g], vv[g], limit, codes=torch.zeros_like(codes[g]), dtype=dtype, ptype=FP)
+            s = torch.where(seen, x @ kk[g].t() / d ** 0.5, torch.tensor(-float("inf"), dtype=torch.float64, device=q.device))
+            most = (torch.softmax(s, 1) * scale[g]).amax(1, keepdim=True)
+            bound[t0:t0 + n, h] = tight + 2.0 ** -25 * most * (seen.double() @ codes[g].abs())
+        t0 += n
+    return o, bound
+
+
+def check8(kernel, n, L, kind, causal, change, H=8, dtype=BF, seed=8, qmul=2.0):
+    """One sequence of L keys, n new tokens, with `change(k, v, ks, vs, at, row)` applied to the cache (at, row: the page and
+    the row of each position)."""
+    g, d, page = gen(seed), 128, 16
+    k, v, ks, vs, table = du.make_cache(g, [L], H, page, d, dtype, kind)
+    pos = torch.arange(L, device="cuda")
+    q = rnd(g, n, H, d, mul=qmul, dtype=dtype)
+    change(q, k, v, ks, vs, table[0].long()[pos // page], pos % page)
+    cache = solattn.PagedCache(k, v, ks, vs)
+    ws = solattn.alloc_paged_workspace(cache, 1, H, n)
+    out = run_on(kernel, lambda: solattn.solattn_paged_forward(q, cache, table, du.cu_of([n]), du.ints([L]), max_new=n,
+                                                               causal=causal, workspace=ws))
+    assert solattn.solattn_get_status(ws) == 0
+    want, bound = paged_oracle8(q, k, v, ks, vs, table, [n], [L], causal, dtype)
+    # the bound means something: an output of zeros would fail in nearly every row that the type can hold (fp16 ends at 2^-24)
+    size = want.abs().amax(2)
+    told = size > (2.0 ** -18 if dtype == FP else 0.0)
+    assert told.double().mean() > 0.5 and (size > 4 * bound.amax(2))[told].double().mean() > 0.9
+    du.check(out, want, bound)
+
+
+KERNELS = [("rows", 15), ("tile", 1000)]
+
+
+@pytest.mark.parametrize("kernel,n", KERNELS)
+@pytest.mark.parametrize("kind", [I8, E4], ids=["int8", "e4m3"])
+@pytest.mark.parametrize("up", [14, 30, 60])
+@pytest.mark.parametrize("where", [9, -2])
+def test_a_later_tokens_scale_leaves_a_row_alone(kernel, n, kind, up, where):
+    """Causal: the value scale of one token is 2^14 to 2^60 times the others'. The tokens in front of it do not see it."""
+    def change(q, k, v, ks, vs, at, row):
+        vs[at[where], :, row[where]] *= 2.0 ** up
+    check8(kernel, n, n, kind, True, change)
+
+
+@pytest.mark.parametrize("kernel,n", KERNELS)
+@pytest.mark.parametrize("kind", [I8, E4], ids=["int8", "e4m3"])
+@pytest.mark.parametrize("where", [0, 200, 699])
+def test_a_large_scale_without_weight_costs_the_others_nothing(kernel, n, kind, where):
+    """A value scale 2^30 times the others', of a key whose score is 2^70 below theirs."""
+    def change(q, k, v, ks, vs, at, row):
+        q[..., 0] = 1.0
+        codes = k.view(torch.uint8)
+        zero, low = torch.tensor([0.0, -112.0], device="cuda").to(kind).view(torch.uint8)
+        codes[..., 0] = zero
+        codes[at[where], :, row[where]] = zero
+        codes[at[where], :, row[where], 0] = low
+        ks[at[where], :, row[where]] = 70 / 1.4427 * 128 ** 0.5 / 112
+        vs[at[where], :, row[where]] *= 2.0 ** 30
+    check8(kernel, n, 1400, kind, False, change, qmul=0.5)
+
+
+@pytest.mark.parametrize("kernel,n", KERNELS)
+@pytest.mark.parametrize("kind", [I8, E4], ids=["int8", "e4m3"])
+@pytest.mark.parametrize("step", [3, -3])
+@pytest.mark.parametrize("dtype", [BF, FP], ids=["bf16", "fp16"])
+def test_scales_that_grow_or_shrink(kernel, n, kind, step, dtype):
+    """Value scales that change eightfold every 70 keys, zeros among them, within fp16's range for fp16."""
+    def change(q, k, v, ks, vs, at, row):
+        pos = torch.arange(len(at), device="cuda")
+        e = (pos // 70) * step
+        e = e - (e.max() + e.min()) // 2 - (6 if dtype == FP else 0)
+        vs[at, :, row] *= torch.exp2(e.float().clamp(-24, 12 if dtype == FP else 40))[:, None]
+        zero = pos % 7 == 0
+        zero[:2] = False
+        vs[at[zero], :, row[zero]] = 0
+        v.view(torch.uint8)[at[zero], :, row[zero]] = 0
+    check8(kernel, n, 1000, kind, True, change, dtype=dtype)
+
+
+@pytest.mark.parametrize("kernel,n", KERNELS)
+@pytest.mark.parametrize("e", [-98, -60, -20, 20, 60, 90])
+def test_caches_of_any_magnitude(kernel, n, e):
+    def change(q, k, v, ks, vs, at, row):
+        vs.mul_(2.0 ** e)
+    check8(kernel, n, 1000, I8, True, change)
+
+
+@pytest.mark.parametrize("kernel,n", KERNELS)
+def test_scales_at_both_ends_of_the_range(kernel, n):
+    """Neighbouring keys 2^180 apart: the small ones count in the sum of weights though their values vanish."""
+    def change(q, k, v, ks, vs, at, row):
+        pos = torch.arange(len(at), device="cuda")
+        vs[at, :, row] *= torch.exp2(torch.where((pos // 150) % 2 == 0, -80.0, 95.0))[:, None]
+    check8(kernel, n, 1000, I8, True, change)
