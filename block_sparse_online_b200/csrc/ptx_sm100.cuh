@@ -432,9 +432,10 @@ __device__ __forceinline__ void exp2_poly_x2(float x0, float x1, float &y0, floa
 }
 
 // The same, except that
-//   * 2^-125 and below is 0 (the clamp's value is subtracted: results from 2^-110 up differ by less than
-//     2^-15 of themselves, from 2^-100 up by nothing), so that a score of -infinity has no weight: 2^-125 is a
-//     normal number, and against values of 2^127, or where nothing else has weight, it would show;
+//   * the lower clamp lies at -127 + 0.003, where the integer sum leaves a subnormal below 2^-134 (about (2^0.003 - 1) 2^-126),
+//     which bf16 and fp16 round to 0: a score of -infinity has no weight. (The 2^-125 of a clamp at -125 is a normal
+//     bf16 and shows against values of 2^120, or where nothing else has weight; subtracting it cost 3 to 6 % of a chunk
+//     of 1560 tokens over 32760 keys.) From -126 up the result is the polynomial's, in between it falls to the clamp's;
 //   * a NaN gives the largest finite number (fmin and fmax would drop it): the clamps hand it through, and the
 //     integer sum below turns its bits into 0x7f7fffff.
 __device__ __forceinline__ void exp2_poly_nan_x2(float x0, float x1, float &y0, float &y1) {
@@ -442,8 +443,8 @@ __device__ __forceinline__ void exp2_poly_nan_x2(float x0, float x1, float &y0, 
   constexpr float c0 = 0.9999280571937561f, c1 = 0.6932609677314758f;
   constexpr float c2 = 0.2426111251115799f, c3 = 0.0551716685295105f;
   float a0, a1;
-  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(a0) : "f"(x0), "f"(-125.f), "f"(126.f));
-  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(a1) : "f"(x1), "f"(-125.f), "f"(126.f));
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(a0) : "f"(x0), "f"(-126.997f), "f"(126.f));
+  asm("{\n\t.reg .f32 t;\n\tmax.NaN.f32 t, %1, %2;\n\tmin.NaN.f32 %0, t, %3;\n\t}" : "=f"(a1) : "f"(x1), "f"(-126.997f), "f"(126.f));
   const uint64_t x = f2(a0, a1);
   const uint64_t t = add2(x, f2(kShift, kShift));
   const uint64_t nf = add2(t, f2(-kShift, -kShift));
@@ -454,11 +455,8 @@ __device__ __forceinline__ void exp2_poly_nan_x2(float x0, float x1, float &y0, 
   float p0, p1, t0, t1;
   f2_split(pp, p0, p1);
   f2_split(t, t0, t1);
-  constexpr float least = -c0 * 0x1p-125f;
-  f2_split(add2(f2(__int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23)),
-                   __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23))),
-                f2(least, least)),
-           y0, y1);
+  y0 = __int_as_float(__float_as_int(p0) + (__float_as_int(t0) << 23));
+  y1 = __int_as_float(__float_as_int(p1) + (__float_as_int(t1) << 23));
 }
 
 __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {

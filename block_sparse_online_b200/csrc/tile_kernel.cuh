@@ -745,8 +745,9 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
 #pragma unroll
         for (int c = 0; c < 2; ++c)
           exp_chunk(c, -ms, acc, std::true_type{});
-        // A maximum of +infinity or NaN makes the row NaN whatever the polynomial made of infinity - infinity.
-        lsum = total(acc) + (ms - ms);
+        // A maximum of +infinity or NaN makes the row NaN whatever the polynomial made of infinity - infinity; where no
+        // key has weight the sum is 0, not the polynomial's least values.
+        lsum = m_ref == -CUDART_INF_F ? 0.f : total(acc) + (ms - ms);
       }
       l = l * grow * grow + lsum;  // (the square may be below 2^-126 where l is above 2^100)
       if (j > 0 && __any_sync(0xffffffffu, grow != 1.f)) {

@@ -375,7 +375,7 @@ int solattn_selftest_exp2(const float *x, float *y, int n, void *stream);
  *              Inputs may overlap or repeat (stride 0); outputs may not
  *   empty rows a query that sees no key gives a row of zeros
  *   rounding   the probabilities (8-bit pages: times the value's scale) are rounded to the product's 16-bit type,
- *              bf16, or fp16 for fp16 and 8-bit pages: off by 2^-9 (2^-12) of their value, or in fp16 by 2^-25 of the row's
+ *              bf16, or fp16 for fp16 and 8-bit pages: off by at most 2^-8 (2^-11) of their value, or in fp16 by 2^-25 of the row's
  *              largest where they are below 2^-14 of it. Sums and outputs are in 32 bits until the last rounding
  *   masked     keys and values behind a sequence's length are not used, whatever they hold.
  *              Keys that only LATER queries see (causal) must have finite values (v)
