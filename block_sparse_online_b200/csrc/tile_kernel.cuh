@@ -79,6 +79,7 @@ struct TileCfg {
                 "control warps give registers up, the others take them");
   static_assert(128 * CTRL_REGS + 256 * SOFTMAX_REGS + (BITS8 ? 128 * CONV_REGS : 0) <= THREADS * LAUNCH_REGS,
                 "register split");
+  static constexpr bool ROW_SCALE = BITS8 && !std::is_same<QT, __half>::value;  // bf16 queries multiply as fp16, far rows by a factor of their own
   static constexpr bool FP16 = std::is_same<MT, __half>::value;
   static constexpr uint32_t IDESC_PV = idesc_16bit_f32(128, D, true, FP16);
 };
@@ -113,6 +114,7 @@ struct TileCtl {
   alignas(16) float lv[C::BITS8 ? C::NSC : 1][C::BITS8 ? 128 : 4];  // their log2_scale()
   alignas(16) float wmax[C::NSC][4];  // largest magnitude of the value scales, by the converter's warps
   uint32_t qmax[2][4];           // converter: largest query of a tile per warp (bf16 bits); tiles alternate
+  int qrel[C::NQ][C::BITS8 ? 128 : 1];  // bf16 queries as fp16: log2 of what a row was divided by over the tile's
 };
 
 template <class C>
@@ -389,11 +391,12 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
     fetch(*g, g->u0, pages, true, cv);
   }
   while (g) {
-    // ---- queries of both halves, a row of each per thread. bf16 queries become fp16 after a division of the
-    // tile by one power of two, which brings its largest finite element to [2^14, 2^15): elements down to
-    // 2^-31 of that are exact, and a smaller one is off by 2^-39 of it, which no logit shows. The factor
-    // goes into the key scales.
-    float up = 1.f, down = 1.f;
+    // ---- queries of both halves, a row of each per thread. bf16 queries become fp16 after a division by a power of
+    // two, which brings the tile's largest finite element to [2^14, 2^15): elements down to 2^-31 of that are exact,
+    // and a smaller one is off by 2^-39 of it. The factor goes into the key scales. A row whose own largest element lies
+    // more than 2^16 below the tile's (another token's, or head's, is that much larger) would lose bits and then
+    // all of them: it is divided by a power of two of its own, and the softmax, which takes its slow path for the warp,
+    // multiplies its scores by the ratio. (A factor for every row in every step: 540 us against 532 for an int8 chunk of 1560 tokens over 32760 keys.)
     const typename C::QT *src[2];
     bool row_ok[2];
 #pragma unroll
@@ -403,8 +406,10 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
       src[w] = static_cast<const typename C::QT *>(a.q) + static_cast<long long>(g->tok + tok) * a.q_tok +
                static_cast<long long>(g->h * a.G + hg) * a.q_head;
     }
-    if constexpr (std::is_same<typename C::QT, __nv_bfloat16>::value) {
-      uint32_t big = 0;
+    float up[2] = {1.f, 1.f}, down = 1.f;
+    int rel[2] = {0, 0};
+    if constexpr (C::ROW_SCALE) {
+      uint32_t big[2] = {0, 0};
 #pragma unroll
       for (int w = 0; w < 2; ++w) {
 #pragma unroll 2
@@ -414,22 +419,28 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
 #pragma unroll
           for (int e = 0; e < 4; ++e) {
             const uint32_t lo = vv[e] & 0x7fffu, hi = (vv[e] >> 16) & 0x7fffu;
-            big = max(big, max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
+            big[w] = max(big[w], max(lo < 0x7f80u ? lo : 0u, hi < 0x7f80u ? hi : 0u));
           }
         }
       }
-      big = __reduce_max_sync(0xffffffffu, big);
+      const uint32_t most = __reduce_max_sync(0xffffffffu, max(big[0], big[1]));
       if (lane == 0) {
-        sc.qmax[item & 1][warp] = big;
+        sc.qmax[item & 1][warp] = most;
         mbar_arrive(&sc.conv);
       }
       if (!wait(&sc.conv, item & 1)) break;
-      big = max(max(sc.qmax[item & 1][0], sc.qmax[item & 1][1]), max(sc.qmax[item & 1][2], sc.qmax[item & 1][3]));
+      const uint32_t *qm = sc.qmax[item & 1];
       ++item;
-      const int ex = static_cast<int>(big >> 7);  // biased exponent
-      const int sh = ex == 0 ? 0 : min(max(141 - ex, -126), 126);
-      up = __int_as_float((127 + sh) << 23);
+      const auto shift = [](int ex) { return ex == 0 ? 0 : min(max(141 - ex, -126), 126); };  // ex: biased exponent
+      const int ex = static_cast<int>(max(max(qm[0], qm[1]), max(qm[2], qm[3])) >> 7), sh = shift(ex);
       down = __int_as_float((127 - sh) << 23);
+#pragma unroll
+      for (int w = 0; w < 2; ++w) {
+        const int own = static_cast<int>(big[w] >> 7);
+        const int sw = own == 0 || own + 16 >= ex ? sh : shift(own);
+        up[w] = __int_as_float((127 + sw) << 23);
+        rel[w] = sh - sw;
+      }
     }
     for (int w = 0; w < 2 && ok; ++w) {
       const int sl = qi % C::NQ;
@@ -439,13 +450,15 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
       for (int i = 0; i < D / 8; ++i) {
         uint4 v = row_ok[w] ? __ldg(reinterpret_cast<const uint4 *>(src[w]) + i) : make_uint4(0, 0, 0, 0);
         if constexpr (std::is_same<typename C::QT, __nv_bfloat16>::value) {
-          v.x = pack_f16x2(__uint_as_float(v.x << 16) * up, __uint_as_float(v.x & 0xffff0000u) * up);
-          v.y = pack_f16x2(__uint_as_float(v.y << 16) * up, __uint_as_float(v.y & 0xffff0000u) * up);
-          v.z = pack_f16x2(__uint_as_float(v.z << 16) * up, __uint_as_float(v.z & 0xffff0000u) * up);
-          v.w = pack_f16x2(__uint_as_float(v.w << 16) * up, __uint_as_float(v.w & 0xffff0000u) * up);
+          const float f = up[w];
+          v.x = pack_f16x2(__uint_as_float(v.x << 16) * f, __uint_as_float(v.x & 0xffff0000u) * f);
+          v.y = pack_f16x2(__uint_as_float(v.y << 16) * f, __uint_as_float(v.y & 0xffff0000u) * f);
+          v.z = pack_f16x2(__uint_as_float(v.z << 16) * f, __uint_as_float(v.z & 0xffff0000u) * f);
+          v.w = pack_f16x2(__uint_as_float(v.w << 16) * f, __uint_as_float(v.w & 0xffff0000u) * f);
         }
         *reinterpret_cast<uint4 *>(dst + swz(tid, i)) = v;
       }
+      sc.qrel[sl][tid] = rel[w];
       publish(&sc.q_full[sl]);
       ++qi;
     }
@@ -635,6 +648,11 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
     const uint32_t qe = qi + w;
     qi += 2;
     float m_ref = -CUDART_INF_F, l = 0.f;
+    bool own_scale = false;  // some row of the warp has a factor of its own
+    if constexpr (C::ROW_SCALE) {
+      if (!wait(&sc.q_full[qe % C::NQ], qe / C::NQ)) break;
+      own_scale = __any_sync(0xffffffffu, sc.qrel[qe % C::NQ][row] != 0);
+    }
     for (int j = 0; j < ns; ++j) {
       const int b = j & 1;
       if (!wait(&sc.s_full[w][b], s_n[b] + (j >> 1))) break;
@@ -716,16 +734,23 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
       bool done = false;
       tmem_wait_ld();
       reg_fence<kStepKeys>(x);
-      if (plain && __all_sync(0xffffffffu, m_ref != -CUDART_INF_F)) {
+      if (plain && !own_scale && __all_sync(0xffffffffu, m_ref != -CUDART_INF_F)) {
         done = exp_fast();
         if (!done) tmem_wait_st();
       }
       if (!done) {
         // With the row maximum (a NaN wins and takes the row): a row's first step, masked steps, and large values.
+        [[maybe_unused]] float f1 = 1.f, g1 = 1.f;
+        if constexpr (C::ROW_SCALE) {  // (two factors: their product may be below 2^-126)
+          const int rel = sc.qrel[qe % C::NQ][row];
+          f1 = __int_as_float((127 + (rel >> 1)) << 23);
+          g1 = __int_as_float((127 + rel - (rel >> 1)) << 23);
+        }
 #pragma unroll
         for (int e = 0; e < kStepKeys; ++e) {
           float f = a.scale_log2;
-          if constexpr (C::BITS8) f = kscale[e];
+          if constexpr (C::ROW_SCALE) f = kscale[e] * f1 * g1;
+          else if constexpr (C::BITS8) f = kscale[e];
           x[e] = e < left ? __float_as_uint(u2f_(x[e]) * f) : __float_as_uint(-CUDART_INF_F);
         }
         float mxs[4] = {-CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F, -CUDART_INF_F};

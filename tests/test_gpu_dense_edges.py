@@ -329,3 +329,28 @@ def test_scales_at_both_ends_of_the_range(kernel, n):
         pos = torch.arange(len(at), device="cuda")
         vs[at, :, row] *= torch.exp2(torch.where((pos // 150) % 2 == 0, -80.0, 95.0))[:, None]
     check8(kernel, n, 1000, I8, True, change)
+
+
+@pytest.mark.parametrize("kernel,n", KERNELS)
+@pytest.mark.parametrize("kind", [None, I8, E4], ids=["16", "int8", "e4m3"])
+@pytest.mark.parametrize("up", [20, 45, 100])
+def test_a_tokens_large_queries_leave_the_others_alone(kernel, n, kind, up):
+    """The queries of one token are 2^20 to 2^100 times the others' (bf16 queries meet 8-bit keys as fp16)."""
+    g, H, d, page, L = gen(9), 8, 128, 16, 1300
+    k, v, ks, vs, table = du.make_cache(g, [L], H, page, d, BF, kind)
+    q = rnd(g, n, H, d, mul=2.0)
+    at = n // 2
+    q[at] *= 2.0 ** up
+    cache = solattn.PagedCache(k, v, ks, vs)
+    out = run_on(kernel, lambda: solattn.solattn_paged_forward(q, cache, table, du.cu_of([n]), du.ints([L]), max_new=n, causal=False))
+    rest = torch.arange(n, device="cuda") != at
+    limit = torch.full((n - 1,), L, device="cuda")
+    for h in range(H):
+        kk, _, _ = du.cached(k, ks, table[0], page, L)
+        vv, codes, cmax = du.cached(v, vs, table[0], page, L)
+        want, bound = du.attend(q[rest, h].double(), kk[h], vv[h], limit, codes=None if codes is None else codes[h], cmax=cmax,
+                                ptype=FP if kind is not None else BF)
+        du.check(out[rest, h], want, bound)
+        # and the token itself chooses one key
+        best = (q[at, h].double() @ kk[h].t()).argmax()
+        du.check(out[at, h], vv[h, best], vv[h, best].abs() * (2.0 ** -7 + 1.5e-4))
