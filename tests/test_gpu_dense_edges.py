@@ -354,3 +354,105 @@ def test_a_tokens_large_queries_leave_the_others_alone(kernel, n, kind, up):
         # and the token itself chooses one key
         best = (q[at, h].double() @ kk[h].t()).argmax()
         du.check(out[at, h], vv[h, best], vv[h, best].abs() * (2.0 ** -7 + 1.5e-4))
+
+
+# ------------------------------------------------------------------ the tile kernel at the ends of its ranges
+
+
+@pytest.mark.parametrize("kernel,n", KERNELS)
+@pytest.mark.parametrize("dtype,kind", [(BF, None), (FP, None), (BF, I8), (BF, E4), (FP, I8)],
+                         ids=["bf16", "fp16", "bf16-int8", "bf16-e4m3", "fp16-int8"])
+@pytest.mark.parametrize("mul,qmul", [(1e-4, 2.0), (30.0, 20.0), (1.0, 0.0)])
+def test_magnitudes(kernel, n, dtype, kind, mul, qmul):
+    """Caches of tiny and large values; logits so large that the softmax is a choice; equal logits."""
+    g, H, d, page = gen(10), 8, 128, 32
+    ns, lens = [n, n], [n + 999, n + 257]
+    k, v, ks, vs, table = du.make_cache(g, lens, H, page, d, dtype, kind, mul=mul)
+    q = rnd(g, 2 * n, H, d, mul=qmul, dtype=dtype)
+    cache = solattn.PagedCache(k, v, ks, vs)
+    ws = solattn.alloc_paged_workspace(cache, 2, H, 2 * n)
+    out = run_on(kernel, lambda: solattn.solattn_paged_forward(q, cache, table, du.cu_of(ns), du.ints(lens), max_new=n, workspace=ws))
+    assert solattn.solattn_get_status(ws) == 0
+    want, bound = du.paged_oracle(q, k, v, ks, vs, table, ns, lens, True, dtype)
+    du.check(out, want, bound)
+
+
+@pytest.mark.parametrize("kernel,n", KERNELS)
+@pytest.mark.parametrize("kind", [None, I8], ids=["16", "int8"])
+def test_offsets_past_32_bits(kernel, n, kind):
+    """A pool of over 2^32 elements: the sequence's pages lie at both ends of it."""
+    d, page, Hkv, pool = 128, 128, 8, 34000
+    assert pool * Hkv * page * d > 1 << 32
+    g = gen(11)
+    k, v = (torch.empty(pool, Hkv, page, d, dtype=kind or BF, device="cuda") for _ in range(2))
+    ks, vs = (None, None) if kind is None else (torch.empty(pool, Hkv, page, device="cuda") for _ in range(2))
+    ids = [pool - 1, 0, pool - 7, 33333, 16500, 1, pool - 2, 32800, 5]
+    for i in ids:
+        for x, s in ((k, ks), (v, vs)):
+            r = rnd(g, Hkv, page, d)
+            if kind is None:
+                x[i] = r
+            else:
+                c, sc = du.quantise(r, kind)
+                x[i], s[i] = c.to(kind), sc
+    table, L = du.ints([ids]), len(ids) * page - 3
+    q = rnd(g, n, Hkv, d)
+    cache = solattn.PagedCache(k, v, ks, vs)
+    out = run_on(kernel, lambda: solattn.solattn_paged_forward(q, cache, table, du.cu_of([n]), du.ints([L]), max_new=n))
+    want, bound = du.paged_oracle(q, k, v, ks, vs, table, [n], [L], True, BF)
+    du.check(out, want, bound)
+
+
+@pytest.mark.parametrize("kernel,n", KERNELS)
+@pytest.mark.parametrize("kind", [None, E4], ids=["16", "e4m3"])
+def test_sequences_that_share_pages(kernel, n, kind):
+    """Sequences behind one prefix: the first pages of each table row are the same; and a table far wider than any of
+    them needs, whose other entries name no page."""
+    g, H, Hkv, d, page = gen(12), 16, 8, 128, 16
+    prefix, ns = 160, [n, 1, n // 2]
+    lens = [prefix + x for x in ns]
+    k, v, ks, vs, table = du.make_cache(g, lens, Hkv, page, d, BF, kind)
+    table[1:, :prefix // page] = table[0, :prefix // page]
+    wide = torch.full((3, 8192), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    q = rnd(g, sum(ns), H, d)
+    cache = solattn.PagedCache(k, v, ks, vs)
+    want, bound = du.paged_oracle(q, k, v, ks, vs, table, ns, lens, True, BF)
+    for t in (table, wide):
+        ws = solattn.alloc_paged_workspace(cache, 3, H, sum(ns))
+        call = lambda: solattn.solattn_paged_forward(q, cache, t, du.cu_of(ns), du.ints(lens), max_new=n, workspace=ws)  # noqa: E731
+        out = run_on(kernel, call) if t is table else call()
+        assert solattn.solattn_get_status(ws) == 0
+        du.check(out, want, bound)
+
+
+@pytest.mark.parametrize("kernel,n", KERNELS)
+@pytest.mark.parametrize("kind", [None, I8], ids=["16", "int8"])
+def test_two_graphs_with_one_workspace(kernel, n, kind):
+    """Two captured calls that share a workspace, replayed in turn on one stream over new lengths and queries."""
+    g, H, Hkv, d, page = gen(13), 8, 8, 128, 64
+    lens = [n + 2000, n + 1, n + 700]
+    ns = [n, 1, n]
+    k, v, ks, vs, table = du.make_cache(g, lens, Hkv, page, d, BF, kind)
+    cache = solattn.PagedCache(k, v, ks, vs)
+    q = [rnd(g, sum(ns), H, d) for _ in range(2)]
+    outs = [torch.empty_like(x) for x in q]
+    cu, length = du.cu_of(ns), du.ints(lens)
+    ws = solattn.alloc_paged_workspace(cache, 3, H, sum(ns))
+    run_on(kernel, lambda: solattn.solattn_paged_forward(q[0], cache, table, cu, length, max_new=n, out=outs[0], workspace=ws))
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for i, graph in enumerate(graphs):
+        with torch.cuda.graph(graph):
+            solattn.solattn_paged_forward(q[i], cache, table, cu, length, max_new=n, causal=i == 0, out=outs[i], workspace=ws)
+    lens2 = [x - 1 if x > n else x for x in lens]
+    length.copy_(du.ints(lens2))
+    q[0].copy_(rnd(g, sum(ns), H, d))
+    torch.cuda.synchronize()
+    for _ in range(4):
+        for graph in graphs:
+            graph.replay()
+    torch.cuda.synchronize()
+    assert solattn.solattn_get_status(ws) == 0
+    for i in range(2):
+        want, bound = du.paged_oracle(q[i], k, v, ks, vs, table, ns, lens2, i == 0, BF)
+        du.check(outs[i], want, bound)
