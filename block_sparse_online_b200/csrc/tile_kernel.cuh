@@ -858,7 +858,8 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
           uint32_t pk[4];
 #pragma unroll
           for (int k = 0; k < 4; ++k) pk[k] = pack16<QT>(u2f_(o[8 * e + 2 * k]) * inv, u2f_(o[8 * e + 2 * k + 1]) * inv);
-          *reinterpret_cast<uint4 *>(buf + swz(row, c * 4 + e)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
+          // (rows behind the half's whole tokens stay zeros: no copy ever fills them)
+          if (my_i < half) *reinterpret_cast<uint4 *>(buf + swz(row, c * 4 + e)) = make_uint4(pk[0], pk[1], pk[2], pk[3]);
         }
       }
       tc_fence_before_sync();
@@ -943,7 +944,8 @@ __global__ void __launch_bounds__(C::THREADS, 1)
     }
   }
   if constexpr (!C::BITS8) {
-    // Rows behind a half's whole tokens are never copied: zeros, so that their scores are finite.
+    // Rows behind a half's whole tokens are never copied and never written again: zeros, so that their scores are finite
+    // (a NaN among them would send its warp down the slow softmax path with every tile).
     const int r0 = (a.tile_tokens >> 1) * a.G, per = (128 - r0) * 8;
     for (int i = threadIdx.x; i < per * C::PANELS * C::NQ; i += C::THREADS) {
       const int pn = i / per, e = i - pn * per;  // panels of the buffers follow one another
