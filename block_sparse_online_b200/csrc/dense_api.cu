@@ -19,7 +19,9 @@ namespace {
 using namespace solattn;
 
 constexpr size_t kHeader = 256;  // [4]: status word
-constexpr unsigned long long kTimeoutNs = 2000000000ull;
+// Limit of a wait on the device. Some last as long as a block's work on one tile (the next queries' buffer, a place for the next
+// segment): 10 us more for each unit of keys that a sequence may have, where a unit takes 1 to 4.
+constexpr unsigned long long kTimeoutNs = 2000000000ull, kTimeoutUnitNs = 10000ull;
 constexpr int kMaxSms = 160;     // blocks per SM slot that the workspace provides for
 constexpr int kRowsBlocks1 = rows_blocks(1) * kMaxSms, kRowsBlocks2 = rows_blocks(2) * kMaxSms;
 
@@ -270,7 +272,7 @@ void set_workspace(DenseArgs *a, void *workspace, int d) {
   a->desc = reinterpret_cast<int4 *>(ws + wl.desc);
   a->part_ml = reinterpret_cast<float *>(ws + wl.ml);
   a->part_o = reinterpret_cast<float *>(ws + wl.o);
-  a->timeout_ns = kTimeoutNs;
+  a->timeout_ns = kTimeoutNs + kTimeoutUnitNs * static_cast<unsigned long long>(a->Lmax / kUnitKeys);
   a->scale_log2 = 1.4426950408889634f / sqrtf(static_cast<float>(d));
 }
 

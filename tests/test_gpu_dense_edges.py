@@ -456,3 +456,24 @@ def test_two_graphs_with_one_workspace(kernel, n, kind):
     for i in range(2):
         want, bound = du.paged_oracle(q[i], k, v, ks, vs, table, ns, lens2, i == 0, BF)
         du.check(outs[i], want, bound)
+
+
+def test_a_tile_that_takes_longer_than_a_wait_may():
+    """2^28 keys (one page, named over and over) for as many tiles as there are SMs: a block is busy with its tile for
+    more than the two seconds of an ordinary wait. (Equal scores: each row is the mean of the page's values, as far as sums of
+    2^28 terms in 32 bits tell.)"""
+    g, d, page, L = gen(14), 64, 128, 1 << 28
+    n = 256 * torch.cuda.get_device_properties(0).multi_processor_count
+    k, v = torch.zeros(1, 1, page, d, dtype=BF, device="cuda"), torch.ones(1, 1, page, d, dtype=BF, device="cuda")
+    q = rnd(g, n, 1, d)
+    table = torch.zeros(1, L // page, dtype=torch.int32, device="cuda")
+    cache = solattn.PagedCache(k, v)
+    ws = solattn.alloc_paged_workspace(cache, 1, 1, n)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    start.record()
+    out = solattn.solattn_paged_forward(q, cache, table, du.cu_of([n]), du.ints([L]), max_new=n, causal=False, workspace=ws)
+    end.record()
+    torch.cuda.synchronize()
+    assert solattn.solattn_get_status(ws) == 0
+    assert start.elapsed_time(end) > 2000, "too quick to show anything: more keys"
+    assert (out > 0).all() and out.isfinite().all()
