@@ -44,6 +44,7 @@
 
 #include <type_traits>
 
+#include "debug_check.cuh"
 #include "ptx_sm100.cuh"
 
 namespace solattn {
@@ -55,7 +56,6 @@ constexpr int kMaskWords = kMaxKeyBlocks / 32;
 constexpr int kPseudoFlag = 0x8000;
 constexpr int kMaxPseudo = kMaxKeyBlocks / 64;
 constexpr int kStatusTimeout = -4;
-constexpr int kStatusBounds = -6;  // a debug-build bounds check failed
 constexpr float kLog2e = 1.4426950408889634f;
 // Lazy rescaling: a row's reference max moves only when the tile max exceeds it by
 // more than this many log2 units, so O is rarely rescaled (P <= 2^8 on the tile that moves
@@ -193,30 +193,6 @@ __device__ __forceinline__ void raise_abort(int *abort_flag, int *status) {
   atomicCAS(status, 0, kStatusTimeout);
   *reinterpret_cast<volatile int *>(abort_flag) = 1;
 }
-
-// Debug builds (-DSOLATTN_DEBUG) check the indices each role derives from shared state
-// before it uses them for a copy, an MMA operand or a store. A failed check records
-// kStatusBounds (if no error is recorded yet) and raises the abort flag; the role then
-// leaves as it does after a timeout, and the other roles follow at their next wait.
-// Release builds compile every check to `true`.
-__device__ __forceinline__ bool debug_fail(int *abort_flag, int *status) {
-  atomicCAS(status, 0, kStatusBounds);
-  *reinterpret_cast<volatile int *>(abort_flag) = 1;
-  return false;
-}
-// Kernels without an abort flag (the routing pass) record the status only; the routing-only
-// entry point runs without a status word (null), and then a failed check only skips the access.
-__device__ __forceinline__ bool debug_fail_status(int *status) {
-  if (status) atomicCAS(status, 0, kStatusBounds);
-  return false;
-}
-#ifdef SOLATTN_DEBUG
-#define SOLATTN_DCHECK(cond, abort_flag, status) ((cond) ? true : debug_fail((abort_flag), (status)))
-#define SOLATTN_DCHECK_STATUS(cond, status) ((cond) ? true : debug_fail_status(status))
-#else
-#define SOLATTN_DCHECK(cond, abort_flag, status) true
-#define SOLATTN_DCHECK_STATUS(cond, status) true
-#endif
 
 __device__ __forceinline__ float u2f(uint32_t x) { return __uint_as_float(x); }
 

@@ -127,6 +127,7 @@ __global__ void __launch_bounds__(kCacheThreads) cache_kernel(const __grid_const
         atomicCAS(a.status, 0, kStatusTable);
       }
       row = pos & (a.page - 1);
+      if (!SOLATTN_DCHECK_STATUS(page < a.num_pages && lo < a.B && tt < a.total && pos < a.Lmax, a.status)) page = -1;
     }
     s_page[threadIdx.x] = page;
     s_row[threadIdx.x] = row;

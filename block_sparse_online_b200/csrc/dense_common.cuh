@@ -24,6 +24,7 @@
 #include <cuda_fp16.h>
 #include <math_constants.h>
 
+#include "debug_check.cuh"
 #include "ptx_sm100.cuh"
 
 namespace solattn {
@@ -60,6 +61,16 @@ struct DenseArgs {
 struct Seq {
   int n, L, tok0;
 };
+
+// What the debug build checks before an access: a row of the queries or the output, a key's place (page or batch, row in it),
+// a partial result's slot.
+__device__ __forceinline__ bool row_inside(const DenseArgs &a, int b, int tok, int head) {
+  return b >= 0 && b < a.B && tok >= 0 && tok < (a.cu ? a.total : a.n) && head >= 0 && head < a.Hkv * a.G;
+}
+__device__ __forceinline__ bool key_inside(const DenseArgs &a, int at, int row) {
+  return at >= 0 && at < (a.table ? a.num_pages : a.B) && row >= 0 && row < (a.table ? a.page : a.Lmax);
+}
+__device__ __forceinline__ bool slot_inside(int slot, int blocks) { return slot >= 0 && slot < 2 * blocks; }
 
 // Query tokens, keys and first query row of sequence b. Values outside the call's buffers
 // are cut to them, so that no access depends on unchecked device data. The cache calls (CacheArgs)
@@ -281,6 +292,7 @@ struct Cursor {
 // Physical page of key position j (a multiple of 16) of sequence b, or -1 (recorded) where
 // the table names no page of the cache: such keys read as zeros.
 __device__ __forceinline__ int page_of(const DenseArgs &a, int b, int j) {
+  if (!SOLATTN_DCHECK_STATUS(b >= 0 && b < a.B && j >= 0 && j < a.Lmax, a.status)) return -1;
   const int id = __ldg(a.table + static_cast<size_t>(b) * a.width + (j >> a.page_shift));
   if (static_cast<unsigned>(id) < static_cast<unsigned>(a.num_pages)) return id;
   atomicCAS(a.status, 0, kStatusTable);
@@ -326,6 +338,7 @@ __global__ void __launch_bounds__(256) join_kernel(const DenseArgs a) {
   const int4 rec = a.desc[c];
   const int parts = rec.x;
   if (parts == 0) return;
+  if (!SOLATTN_DCHECK_STATUS(parts > 0 && c + parts <= static_cast<int>(gridDim.x) && rec.y >= 0 && rec.y < a.B, a.status)) return;
   const Seq s = seq_of(a, rec.y);
   if constexpr (T::RT == TokenTiles::RT) {
     // Parts lie column group by column group: a warp reads 32 rows of a group of 4 columns
@@ -356,6 +369,7 @@ __global__ void __launch_bounds__(256) join_kernel(const DenseArgs a) {
       const int rl = i / (D / 4), e = i % (D / 4);
       int tok, g;
       if (!T::row(a, s.n, rec.w, blockIdx.y * ROWS + rl, tok, g)) continue;
+      if (!SOLATTN_DCHECK_STATUS(row_inside(a, rec.y, s.tok0 + tok, rec.z * a.G + g), a.status)) continue;
       QT *dst = static_cast<QT *>(a.out) + rec.y * a.o_batch + static_cast<long long>(s.tok0 + tok) * a.o_tok +
                 static_cast<long long>(rec.z * a.G + g) * a.o_head + 4 * e;
       *reinterpret_cast<uint2 *>(dst) = out[rl][e];
@@ -370,6 +384,7 @@ __global__ void __launch_bounds__(256) join_kernel(const DenseArgs a) {
     const int r = blockIdx.y * ROWS + i;
     int tok, g;
     if (!T::row(a, s.n, rec.w, r, tok, g)) continue;
+    if (!SOLATTN_DCHECK_STATUS(row_inside(a, rec.y, s.tok0 + tok, rec.z * a.G + g), a.status)) continue;
     float m = -CUDART_INF_F, l = 0.f, o[CPL];
 #pragma unroll
     for (int e = 0; e < CPL; ++e) o[e] = 0.f;

@@ -154,7 +154,8 @@ __global__ void __launch_bounds__(kRowsWarps * 32, rows_blocks(NT)) rows_kernel(
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt) {
       int tok, gg;
-      const bool ok = T::row(a, s.n, t, nt * 8 + g, tok, gg);
+      const bool ok = T::row(a, s.n, t, nt * 8 + g, tok, gg) &&
+                      SOLATTN_DCHECK_STATUS(row_inside(a, b, s.tok0 + tok, h * a.G + gg), a.status);
       const QT *src = static_cast<const QT *>(a.q) + b * a.q_batch + static_cast<long long>(s.tok0 + tok) * a.q_tok +
                       static_cast<long long>(h * a.G + gg) * a.q_head;
       uint32_t w[D / 8];
@@ -219,7 +220,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, rows_blocks(NT)) rows_kernel(
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int key = gr * 16 + g + 8 * e;
-        const bool ok = id >= 0 && key < klim;
+        const bool ok = id >= 0 && key < klim && SOLATTN_DCHECK_STATUS(key_inside(a, id, j + g + 8 * e), a.status);
         const uint8_t *p = kbase + (id * a.k_seq + static_cast<long long>(j + g + 8 * e) * a.k_row) * ES + c * 16;
 #pragma unroll
         for (int i = 0; i < C::KW / 4; ++i) {
@@ -239,7 +240,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, rows_blocks(NT)) rows_kernel(
 #pragma unroll
       for (int e = 0; e < 4; ++e) {
         const int kk = 2 * c + (e & 1) + 8 * (e >> 1);  // keys 2c, 2c+1, 2c+8, 2c+9
-        const bool ok = id >= 0 && gr * 16 + kk < klim;
+        const bool ok = id >= 0 && gr * 16 + kk < klim && SOLATTN_DCHECK_STATUS(key_inside(a, id, j + kk), a.status);
         const uint8_t *p = vbase + (id * a.v_seq + static_cast<long long>(j + kk) * a.v_row) * ES;
         if constexpr (C::VW == 8) {  // 16 bits, d = 128: two pieces 64 columns apart
 #pragma unroll
@@ -412,6 +413,7 @@ __global__ void __launch_bounds__(kRowsWarps * 32, rows_blocks(NT)) rows_kernel(
     for (int r = threadIdx.x / TPR; r < C::ROWS; r += kRowsWarps * 32 / TPR) {
       int tok, gg;
       if (!T::row(a, s.n, t, r, tok, gg)) continue;
+      if (!SOLATTN_DCHECK_STATUS(row_inside(a, b, s.tok0 + tok, h * a.G + gg) && slot_inside(slot, gridDim.x), a.status)) continue;
       float mm = -CUDART_INF_F;
 #pragma unroll
       for (int w = 0; w < kRowsWarps; ++w) mm = fmaxf(mm, sm.m[w][r]);

@@ -185,6 +185,10 @@ __device__ void tile_scheduler(TileCtl<C> &sc, const DenseArgs &a, const TileArg
       g.lim0 = a.causal ? s.L - s.n + cur.t * a.tile_tokens + 1 : s.L;
       g.part = cur.partial() ? cur.slot(blockIdx.x) : -1;
       if (cur.partial() && cur.u0 == 0) rec = cur.record(blockIdx.x);
+      if (!SOLATTN_DCHECK(g.n > 0 && g.u0 >= 0 && (g.u0 + g.n - 1) * kUnitKeys <= a.Lmax && g.klim <= g.L && row_inside(a, g.b, g.tok, g.h * a.G) &&
+                              g.end <= (a.cu ? a.total : a.n) && (g.part < 0 || slot_inside(g.part, gridDim.x)),
+                          &sc.abort_flag, a.status))
+        break;
     }
     sc.seg[sl] = g;
     mbar_arrive(&sc.seg_full[sl]);
@@ -330,7 +334,7 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
   // behind the sequence's end. Read a unit ahead of the codes, and looked at only then.
   auto fetch_entries = [&](const Segment &c, int u) {
     const int j = u * kUnitKeys + (lane & 7) * 16;
-    return j < c.L ? __ldg(a.table + static_cast<size_t>(c.b) * a.width + (j >> a.page_shift)) : -2;
+    return j < c.L && SOLATTN_DCHECK(j < a.Lmax, &sc.abort_flag, a.status) ? __ldg(a.table + static_cast<size_t>(c.b) * a.width + (j >> a.page_shift)) : -2;
   };
   // The pages they name; -1 for none (an entry that names no page of the cache is recorded).
   auto pages_of = [&](int entry) {
@@ -346,14 +350,14 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
     for (int i = 0; i < NP; ++i) {
       const int j = u * kUnitKeys + i * RPP + rl;
       const int id = __shfl_sync(0xffffffffu, pages, (i * RPP + rl) >> 4);
-      cd[i] = id >= 0 && j < c.L ? ld_stream16(base + id * seq + (j & (a.page - 1)) * row) : make_uint4(0, 0, 0, 0);
+      cd[i] = id >= 0 && j < c.L && SOLATTN_DCHECK(key_inside(a, id, j & (a.page - 1)), &sc.abort_flag, a.status) ? ld_stream16(base + id * seq + (j & (a.page - 1)) * row) : make_uint4(0, 0, 0, 0);
     }
   };
   // The scales of a unit: thread t takes key t.
   auto fetch_scales = [&](const Segment &c, int u, int pages) {
     const int j = u * kUnitKeys + tid;
     const int id = __shfl_sync(0xffffffffu, pages, tid >> 4);
-    const bool in = id >= 0 && j < c.L;
+    const bool in = id >= 0 && j < c.L && SOLATTN_DCHECK(key_inside(a, id, j & (a.page - 1)), &sc.abort_flag, a.status);
     const size_t at = (static_cast<size_t>(max(id, 0)) * a.Hkv + c.h) * a.page + (j & (a.page - 1));
     ksc = in ? __ldg(a.k_scale + at) : 0.f;
     vsc = in ? __ldg(a.v_scale + at) : 0.f;
@@ -402,7 +406,8 @@ __device__ void tile_converter(TileCtl<C> &sc, const DenseArgs &a, uint8_t *q_sm
 #pragma unroll
     for (int w = 0; w < 2; ++w) {
       int tok, hg;
-      row_ok[w] = half_row(a, *g, w, tid, tok, hg);
+      row_ok[w] = half_row(a, *g, w, tid, tok, hg) &&
+                  SOLATTN_DCHECK(row_inside(a, g->b, g->tok + tok, g->h * a.G + hg), &sc.abort_flag, a.status);
       src[w] = static_cast<const typename C::QT *>(a.q) + static_cast<long long>(g->tok + tok) * a.q_tok +
                static_cast<long long>(g->h * a.G + hg) * a.q_head;
     }
@@ -867,7 +872,7 @@ __device__ void tile_softmax(TileCtl<C> &sc, const DenseArgs &a, uint32_t tmem, 
       unsigned long long dst = reinterpret_cast<unsigned long long>(
           static_cast<QT *>(a.out) + sg->b * a.o_batch + static_cast<long long>(sg->tok + my_tok) * a.o_tok +
           static_cast<long long>(sg->h * a.G + my_hg) * a.o_head);
-      if (!row_in(*sg)) dst = 0;
+      if (!row_in(*sg) || !SOLATTN_DCHECK(row_inside(a, sg->b, sg->tok + my_tok, sg->h * a.G + my_hg), &sc.abort_flag, a.status)) dst = 0;
       __syncwarp();
       constexpr int LPR = D / 8, RPI = 32 / LPR;  // lanes of a row, rows of a store
       const int ch = lane % LPR;

@@ -20,3 +20,10 @@ def test_a_status_word_needs_its_256_bytes(log, bytes_, dtype):  # noqa: F811
     assert log["launch"] == []
     solattn.solattn_cache_append(paged_cache(), rows(4, 2, 64), rows(4, 2, 64), *args, workspace=on_gpu(torch.zeros(256, dtype=dtype)))
     assert log["launch"] == [11]
+
+
+@pytest.mark.parametrize("name", ["dense_common", "rows_kernel", "tile_kernel", "cache_kernel", "attn_kernel"])
+def test_kernels_have_the_debug_builds_checks(name):
+    """libsolattn_debug.so promises checks of the indices before an access, in every kernel."""
+    src = open(solattn.library_path().rsplit("/", 1)[0] + f"/csrc/{name}.cuh").read()
+    assert "SOLATTN_DCHECK" in src
