@@ -8,7 +8,9 @@ One step is one solattn_forward call (block pooling + the fused routed
 attention kernel) over one batch of synthetic spatio-temporal Q/K/V of the
 named configuration, inputs resident in HBM. The headline workload is the 480p
 video shape (B=1, H=12, N=32760, d=128, 128x128 blocks), keep_correct at tau=6.
-Prints ONE JSON line (rank 0). Multi-GPU runs are independent replicas (weak
+Prints ONE JSON line (rank 0) on standard output; the sweeps over modes, thresholds and
+configurations go to standard error as a JSON line of their own (they take 20 KB, and what
+keeps only the end of the output would lose the head of the line). Multi-GPU runs are independent replicas (weak
 scaling): the operator has no cross-GPU exchange.
 
 ``--impl reference`` times the fp64 CPU oracle on a bounded sample of the same
@@ -293,6 +295,12 @@ def config_dict(args, cfg, world):
             "B": B, "H": H, "N": N, "d": d, "Bq": cfg.Bq, "Bk": cfg.Bk,
             "l2": "inputs larger than L2 (q, k, v = %.0f MB)" % (3 * elem * 2 / 1e6),
             "parallelism": f"replicas x{world}"}
+
+
+def emit(line, details):
+    """The result on standard output, what belongs to it on standard error."""
+    print(json.dumps({"details": details}), file=sys.stderr, flush=True)
+    print(json.dumps(line), flush=True)
 
 
 def reference_arm(args, world, rank):
@@ -673,11 +681,8 @@ def main():
             "gpu_launches": args.steps * (2 if args.mode == "dense" else 3),
             "clocks": clk,
             "cpu_baseline": cpu,
-            "sweep": sweep,
-            "routing_overhead": routing,
-            "configs": configs,
         }
-        print(json.dumps(line), flush=True)
+        emit(line, {"sweep": sweep, "routing_overhead": routing, "configs": configs})
     if world > 1:
         dist.destroy_process_group()
 
