@@ -2,7 +2,7 @@
 //
 // These calls take 3 to 10 us on the GPU at the sizes of single tokens, and checking a call's
 // tensors attribute by attribute in Python takes as long. The functions here check the usual
-// call (every tensor given, on the current device, on the current stream) and make it. They
+// call (every tensor given, on the current device, on the current stream or a given one of that device) and make it. They
 // return the library's status, or None for anything else: the caller then takes the Python way, which
 // says what is wrong or does what is left. The library's function is passed as an address, so
 // that a call goes to the library that the Python side has loaded.
@@ -65,9 +65,23 @@ void *address(PyObject *x) { return PyLong_AsVoidPtr(x); }
 
 PyObject *status(int rc) { return PyLong_FromLong(rc); }
 
-// (function, q, k, v, key_len or None, out, workspace)
+// The call's stream: the current one for None, else that of a torch.cuda.Stream of the device.
+bool stream_of(PyObject *s, int dev, void **out) {
+  if (s == Py_None) {
+    *out = c10::cuda::getCurrentCUDAStream(dev).stream();
+    return true;
+  }
+  PyObject *d = PyObject_GetAttrString(s, "device_index"), *h = d ? PyObject_GetAttrString(s, "cuda_stream") : nullptr;
+  const bool ok = h && PyLong_Check(d) && PyLong_Check(h) && PyLong_AsLong(d) == dev;
+  if (ok) *out = PyLong_AsVoidPtr(h);
+  Py_XDECREF(d);
+  Py_XDECREF(h);
+  return ok && !PyErr_Occurred();
+}
+
+// (function, q, k, v, key_len or None, out, workspace, stream or None)
 PyObject *cross(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  if (n != 7) Py_RETURN_NONE;
+  if (n != 8) Py_RETURN_NONE;
   const at::Tensor *q = tensor(a[1]), *k = tensor(a[2]);
   if (!q || !k || !q->is_cuda() || q->dim() != 4 || k->dim() != 4) Py_RETURN_NONE;
   const int dev = q->get_device(), dt = dtype_of(*q);
@@ -76,22 +90,21 @@ PyObject *cross(PyObject *, PyObject *const *a, Py_ssize_t n) {
   for (int64_t x : {s[0], s[1], s[2], s[3], ks[1], ks[2]})
     if (x > INT32_MAX) Py_RETURN_NONE;
   solattn_view vq, vk, vv, vo;
-  void *ws;
+  void *ws, *st;
   size_t wn;
   const int32_t *len = nullptr;
   if (!view(a[1], dev, dt, 4, s[0], s[1], s[2], s[3], &vq) || !view(a[2], dev, dt, 4, s[0], ks[1], ks[2], s[3], &vk) ||
       !view(a[3], dev, dt, 4, s[0], ks[1], ks[2], s[3], &vv) || !view(a[5], dev, dt, 4, s[0], s[1], s[2], s[3], &vo) ||
-      !bytes(a[6], dev, &ws, &wn) || (a[4] != Py_None && !(len = ints(a[4], dev, s[0]))))
+      !bytes(a[6], dev, &ws, &wn) || (a[4] != Py_None && !(len = ints(a[4], dev, s[0]))) || !stream_of(a[7], dev, &st))
     Py_RETURN_NONE;
   const auto fn = reinterpret_cast<decltype(&solattn_cross)>(address(a[0]));
   return status(fn(&vq, &vk, &vv, &vo, len, static_cast<int>(s[0]), static_cast<int>(s[1]), static_cast<int>(ks[1]),
-                   static_cast<int>(s[2]), static_cast<int>(ks[2]), static_cast<int>(s[3]), dt, ws, wn,
-                   c10::cuda::getCurrentCUDAStream(dev).stream()));
+                   static_cast<int>(s[2]), static_cast<int>(ks[2]), static_cast<int>(s[3]), dt, ws, wn, st));
 }
 
-// (function, cache, its device, its 16-bit dtype or -1, q, table, cu, length, max_new, causal, out, workspace)
+// (function, cache, its device, its 16-bit dtype or -1, q, table, cu, length, max_new, causal, out, workspace, stream or None)
 PyObject *paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  if (n != 12) Py_RETURN_NONE;
+  if (n != 13) Py_RETURN_NONE;
   const auto *c = static_cast<const solattn_cache *>(address(a[1]));
   const int dev = static_cast<int>(PyLong_AsLong(a[2])), cdt = static_cast<int>(PyLong_AsLong(a[3]));
   const at::Tensor *q = tensor(a[4]);
@@ -104,22 +117,21 @@ PyObject *paged(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const int causal = PyObject_IsTrue(a[9]);
   solattn_seqs s;
   solattn_view vq, vo;
-  void *ws;
+  void *ws, *st;
   size_t wn;
   if (over || max_new < 0 || max_new > INT32_MAX || causal < 0 || H > INT32_MAX || !seqs(a[5], a[6], a[7], dev, total, &s) ||
       !view(a[4], dev, dt, 3, 1, H, total, c->d, &vq) || !view(a[10], dev, dt, 3, 1, H, total, c->d, &vo) ||
-      !bytes(a[11], dev, &ws, &wn)) {
+      !bytes(a[11], dev, &ws, &wn) || !stream_of(a[12], dev, &st)) {
     PyErr_Clear();
     Py_RETURN_NONE;
   }
   const auto fn = reinterpret_cast<decltype(&solattn_paged_forward)>(address(a[0]));
-  return status(fn(&vq, &vo, c, &s, static_cast<int>(H), static_cast<int>(max_new), causal, dt, ws, wn,
-                   c10::cuda::getCurrentCUDAStream(dev).stream()));
+  return status(fn(&vq, &vo, c, &s, static_cast<int>(H), static_cast<int>(max_new), causal, dt, ws, wn, st));
 }
 
-// (function, write, cache, its device, its 16-bit dtype or -1, k rows, v rows, table, cu, length, workspace)
+// (function, write, cache, its device, its 16-bit dtype or -1, k rows, v rows, table, cu, length, workspace, stream or None)
 PyObject *cache_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
-  if (n != 11) Py_RETURN_NONE;
+  if (n != 12) Py_RETURN_NONE;
   const auto *c = static_cast<const solattn_cache *>(address(a[2]));
   const int dev = static_cast<int>(PyLong_AsLong(a[3])), cdt = static_cast<int>(PyLong_AsLong(a[4]));
   const at::Tensor *k = tensor(a[5]);
@@ -129,12 +141,11 @@ PyObject *cache_rows(PyObject *, PyObject *const *a, Py_ssize_t n) {
   const int64_t total = k->size(0);
   solattn_seqs s;
   solattn_view vk, vv;
-  void *ws;
+  void *ws, *st;
   size_t wn;
   if (!seqs(a[7], a[8], a[9], dev, total, &s) || !view(a[5], dev, dt, 3, 1, c->Hkv, total, c->d, &vk) ||
-      !view(a[6], dev, dt, 3, 1, c->Hkv, total, c->d, &vv) || !bytes(a[10], dev, &ws, &wn) || wn < 256)
+      !view(a[6], dev, dt, 3, 1, c->Hkv, total, c->d, &vv) || !bytes(a[10], dev, &ws, &wn) || wn < 256 || !stream_of(a[11], dev, &st))
     Py_RETURN_NONE;
-  void *st = c10::cuda::getCurrentCUDAStream(dev).stream();
   if (a[1] == Py_True) return status(reinterpret_cast<decltype(&solattn_cache_append)>(address(a[0]))(c, &vk, &vv, &s, dt, ws, st));
   return status(reinterpret_cast<decltype(&solattn_cache_read)>(address(a[0]))(c, &s, &vk, &vv, dt, ws, st));
 }

@@ -197,13 +197,21 @@ def _on_stream(fn):
         stream = args[at] if len(args) > at else kw.get("stream")
         if stream is None:
             return fn(*args, **kw)
-        with torch.cuda.stream(stream):
-            result = fn(*args, **kw)
         caller = torch.cuda.current_stream(stream.device)
-        if caller != stream:
-            for t in result if isinstance(result, tuple) else (result,):
-                if isinstance(t, torch.Tensor) and t.is_cuda:
-                    t.record_stream(caller)
+        if caller == stream:
+            return fn(*args, **kw)
+        if _current_device() == stream.device.index:  # (the context manager takes twice as long)
+            torch.cuda.set_stream(stream)
+            try:
+                result = fn(*args, **kw)
+            finally:
+                torch.cuda.set_stream(caller)
+        else:
+            with torch.cuda.stream(stream):
+                result = fn(*args, **kw)
+        for t in result if isinstance(result, tuple) else (result,):
+            if isinstance(t, torch.Tensor) and t.is_cuda:
+                t.record_stream(caller)
         return result
 
     return call
@@ -645,8 +653,8 @@ def solattn_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_len: to
     may hold anything); a sequence of none gives zeros. H is a multiple of Hkv: query head h
     uses key head h // (H // Hkv). Returns out [B, H, Nq, d]. Asynchronous on ``stream``;
     lengths outside [0, Nk] are reported by :func:`solattn_get_status` on the workspace."""
-    if stream is None and _fast is not None:
-        rc = _fast.cross(_at["solattn_cross"], q, k, v, key_len, out, workspace)
+    if _fast is not None:
+        rc = _fast.cross(_at["solattn_cross"], q, k, v, key_len, out, workspace, stream)
         if rc is not None:
             if rc:
                 _check(rc, "solattn_cross")
@@ -744,8 +752,9 @@ def solattn_paged_forward(q: torch.Tensor, cache: PagedCache, table: torch.Tenso
     Lengths or pages out of range are reported by :func:`solattn_get_status` on the workspace."""
     if not isinstance(cache, PagedCache):
         raise ValueError("cache must be a PagedCache")
-    if stream is None and _fast is not None:
-        rc = _fast.paged(_at["solattn_paged_forward"], *cache._fast, q, table, cu, length, max_new, causal, out, workspace)
+    if _fast is not None:
+        rc = _fast.paged(_at["solattn_paged_forward"], *cache._fast, q, table, cu, length, max_new, causal, out, workspace,
+                         stream)
         if rc is not None:
             if rc:
                 _check(rc, "solattn_paged_forward")
@@ -776,8 +785,9 @@ def solattn_cache_append(cache: PagedCache, new_k: torch.Tensor, new_v: torch.Te
     quantised where the cache is 8-bit: scale = max|x| / TOP, code = nearest(x TOP / max|x|), TOP = 127
     (int8) or 448 (e4m3). table, cu, length as in :func:`solattn_paged_forward` (length counts
     the new tokens). ``workspace``: an :func:`alloc_status` tensor or any workspace."""
-    if stream is None and _fast is not None:
-        rc = _fast.cache_rows(_at["solattn_cache_append"], True, *cache._fast, new_k, new_v, table, cu, length, workspace)
+    if _fast is not None:
+        rc = _fast.cache_rows(_at["solattn_cache_append"], True, *cache._fast, new_k, new_v, table, cu, length, workspace,
+                              stream)
         if rc is not None:
             if rc:
                 _check(rc, "solattn_cache_append")
@@ -800,8 +810,9 @@ def solattn_cache_read(cache: PagedCache, table: torch.Tensor, cu: torch.Tensor,
                        k_out: torch.Tensor, v_out: torch.Tensor, workspace: torch.Tensor | None = None, stream=None):
     """Reads the new tokens' rows (the last cu[b+1] - cu[b] of each sequence) back from the pages into
     k_out and v_out [total, Hkv, d] (bf16 or fp16): code * scale, rounded once. Returns them."""
-    if stream is None and _fast is not None:
-        rc = _fast.cache_rows(_at["solattn_cache_read"], False, *cache._fast, k_out, v_out, table, cu, length, workspace)
+    if _fast is not None:
+        rc = _fast.cache_rows(_at["solattn_cache_read"], False, *cache._fast, k_out, v_out, table, cu, length, workspace,
+                              stream)
         if rc is not None:
             if rc:
                 _check(rc, "solattn_cache_read")

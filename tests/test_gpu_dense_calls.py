@@ -98,3 +98,44 @@ def test_operator_stream_without_workspace():
     overwrite(need)
     torch.cuda.synchronize()
     assert torch.equal(out, want) and torch.equal(kept, kept2)
+
+
+def test_everything_given_on_a_stream():
+    """With every tensor given a call takes the short path on a given stream too: it is queued there, not on the current one."""
+    g, H, d, page, L, n = gen(104), 4, 128, 16, 300, 5
+    q, k, v = (rnd(g, 1, H, m, d) for m in (n, L, L))
+    kp, vp, ks, vs, table = du.make_cache(g, [L], H, page, d, BF, torch.int8)
+    cache = solattn.PagedCache(kp, vp, ks, vs)
+    cu, length = du.cu_of([n]), du.ints([L])
+    pq, new = rnd(g, n, H, d), rnd(g, n, H, d)
+    outs = [torch.zeros_like(x) for x in (q, pq, new, new)]
+    ws, pws = solattn.alloc_cross_workspace(1, H, H, n, L, d), solattn.alloc_paged_workspace(cache, 1, H, n)
+    s = torch.cuda.Stream()
+
+    def calls():
+        solattn.solattn_cross(q, k, v, out=outs[0], workspace=ws, stream=s)
+        solattn.solattn_cache_append(cache, new, new, table, cu, length, workspace=pws, stream=s)
+        solattn.solattn_paged_forward(pq, cache, table, cu, length, n, True, outs[1], pws, s)
+        solattn.solattn_cache_read(cache, table, cu, length, outs[2], outs[3], workspace=pws, stream=s)
+
+    torch.cuda.synchronize()
+    calls()  # loads the kernels
+    torch.cuda.synchronize()
+    assert not any(bool((x == 0).all()) for x in outs)
+    for x in outs:
+        x.zero_()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(s):
+        torch.cuda._sleep(500_000_000)  # about a quarter of a second
+    calls()
+    torch.cuda.current_stream().synchronize()
+    early = [bool((x == 0).all()) for x in outs]
+    s.synchronize()
+    assert all(early) and solattn.solattn_get_status(ws) == 0 and solattn.solattn_get_status(pws) == 0
+    want, bound = du.cross_oracle(q, k, v, None, BF)
+    du.check(outs[0], want, bound)
+    want, bound = du.paged_oracle(pq, kp, vp, ks, vs, table, [n], [L], True, BF)
+    du.check(outs[1], want, bound)
+    codes, sc = du.quantise(new, torch.int8)
+    for x in outs[2:]:
+        assert torch.equal(x, (codes.float() * sc[..., None]).to(BF))

@@ -37,8 +37,10 @@ def log(monkeypatch):
     @contextlib.contextmanager
     def stream(s):
         active.append(s)
-        yield
-        active.pop()
+        try:
+            yield
+        finally:
+            active.pop()
 
     def made(fn):
         def call(*a, device=None, **kw):
@@ -61,6 +63,7 @@ def log(monkeypatch):
     monkeypatch.setattr(torch, "empty_like", made(lambda x, **kw: real_empty(x.shape, dtype=x.dtype)))
     monkeypatch.setattr(OnGpu, "zero_", lambda x: (seen["clear"].append(active[-1].cuda_stream), real_zero(x))[1], raising=False)
     monkeypatch.setattr(torch.cuda, "stream", stream)
+    monkeypatch.setattr(torch.cuda, "set_stream", lambda s: active.__setitem__(-1, s))
     monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: active[-1])
     monkeypatch.setattr(torch.cuda, "device", lambda device: contextlib.nullcontext())
     monkeypatch.setattr(solattn, "_current_device", lambda: 0)
@@ -115,6 +118,17 @@ def test_memory_belongs_to_the_stream_of_the_launch(name, log):
 def test_without_a_stream_all_is_on_the_current_one(name, log):
     CALLS[name](None)
     assert log["launch"] == [11] and set(log["alloc"]) == {11} and set(log["clear"]) <= {11}
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_the_current_stream_is_put_back(log, monkeypatch, current):
+    """After the call and after a refusal, whichever device is current."""
+    monkeypatch.setattr(solattn, "_current_device", lambda: current)
+    CALLS["cross"](SIDE)
+    assert torch.cuda.current_stream() is CURRENT
+    with pytest.raises(ValueError):
+        solattn.solattn_cross(rows(1, 2, 5, 64), rows(1, 2, 7, 64), rows(1, 2, 8, 64), stream=SIDE)
+    assert torch.cuda.current_stream() is CURRENT
 
 
 def test_a_stream_of_another_device_is_refused(log):
