@@ -8,8 +8,8 @@
 // The code is the one nearest to the exact ratio: x_e TOP is exact in fp32 (11 bits by 7)
 // and a ratio that is no tie lies at least 2^-19 of itself from one, so an fp32 quotient that
 // is exact for short ratios and near for the others falls on the right side of it: the product
-// with the row's reciprocal (off by 2^-22), corrected once by its residual, is off by 2^-45 before
-// its last rounding. (Dividing by the ROUNDED scale turns ties to one side; a full division
+// with the row's reciprocal (off by 2^-22), corrected once by its residual (Markstein's step of a division by
+// multiplication, 1990), is off by 2^-45 before its last rounding. (Dividing by the ROUNDED scale turns ties to one side; a full division
 // for each element cost 14 us where the row's reciprocal and two more products cost 6: 1560 tokens of
 // 12 heads of 128.)
 // Read back: fl16(code_e scale), one rounding.
@@ -21,7 +21,8 @@
 // holds pieces of 8 elements (one 16-byte access of 16-bit data): one piece when writing, where the
 // row's maximum takes shuffles and the quotients registers, two when reading. 75600 e4m3 tokens of 24 heads of 128
 // are read back in 240 us (1.41 GB, 5.8 TB/s; the card's copy runs at 6.55); 1560 int8 tokens of 12 heads
-// are written in 8.7 us and read back in 6.1, which is mostly launch and the way from token to page.
+// are written in 7.3 us and read back in 4.6 (activity records), which is mostly launch, the way from token to page
+// and, when writing, three turns whose rows are loaded one turn after the other.
 #pragma once
 
 #include "dense_common.cuh"

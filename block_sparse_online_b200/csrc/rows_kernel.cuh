@@ -32,7 +32,7 @@
 // [2^14, 2^15): exact down to 2^-31 of that element.
 //
 // Bound by memory: at 32 sequences of 1 to 16384 keys, 4 key heads of 128, bf16, one token each, it reads
-// 551 MB in 85.5 us (6.4 TB/s). In e4m3 at 118800 keys of 24 heads (753 MB) it takes 141 us (5.3 TB/s): half the
+// 551 MB in 84 us (6.5 TB/s). In e4m3 at 118800 keys of 24 heads (753 MB) it takes 135 us (5.6 TB/s): half the
 // bytes for each key leave half the bytes in flight, and more blocks per SM cost spills. Measured and not kept:
 // the next values loaded before the next scores (155 us there), four blocks per SM (156 us).
 #pragma once
@@ -113,7 +113,9 @@ __device__ __forceinline__ float log2_scale(float x) { return fminf(fmaxf(__log2
 constexpr int kRowsWarps = 4;
 constexpr float kRowsSlack = 8.0f;  // log2 units the reference maximum may lag
 
-// Blocks of an SM, as registers allow (four for the 8-bit kinds spill: 156 against 142 us at 118800 e4m3 keys of 24 heads).
+// Blocks of an SM, as registers allow: 168 of a thread with eight rows, 254 with sixteen. (The 16-bit kernel for d = 128 and
+// eight rows stores 32 to 72 bytes of a thread to local memory at that; four blocks for the 8-bit kinds
+// spill more: 156 against 142 us at 118800 e4m3 keys of 24 heads.)
 constexpr int rows_blocks(int nt) { return nt == 1 ? 3 : 2; }
 
 template <class QT, int KIND, int D, int NT, bool PAGED>

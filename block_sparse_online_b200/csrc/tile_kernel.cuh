@@ -29,14 +29,15 @@
 // the reference is that of x + log2 |value scale|, as in the rows kernel; that no product of P and a scale is
 // large is shown by the row sum times the unit's largest scale.
 //
-// What bounds it, measured at 1560 tokens x 32760 keys x 12 heads of 128 in bf16 (350 to 400 us, 800 to 900
+// What bounds it, measured at 1560 tokens x 32760 keys x 12 heads of 128 in bf16 (320 to 400 us, 800 to 980
 // TFLOP/s; the card's power limit moves it): the tensor core's instructions. A step's 8 products of 64 columns
 // take 85 cycles each where 128 columns take 67, so a step costs both halves 1900 cycles, the
 // softmax 1700. Measured and not kept: one S buffer of 128 columns with two warpgroups a half by columns
 // (387 us), two warpgroups a half by steps (400 us), output by TMA stores (no gain, and the queries'
 // buffer comes back late), a deeper queue of queries for a shallower ring of keys (558 us). Short rows of
 // keys (one or two steps) are bound by a tile's fixed 5500 cycles: queries in, first maximum, rows out.
-// 8-bit caches add the expansion of the codes, which is what bounds them (540 to 560 us for the same in int8).
+// 8-bit caches add the expansion of the codes, which is what bounds them (520 to 550 us for the same in int8; every tile
+// expands its keys again, and the softmax warps store 52 to 88 bytes of a thread for want of registers).
 //
 // Causal and ragged ends: columns at or behind a row's limit are replaced by -infinity; the
 // products of a unit stop at the last 16 keys that some row of the tile sees.

@@ -652,7 +652,9 @@ def solattn_cross(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, key_len: to
     ``key_len``: int32 [B] on the device, the keys of each sequence (the rest is padding that
     may hold anything); a sequence of none gives zeros. H is a multiple of Hkv: query head h
     uses key head h // (H // Hkv). Returns out [B, H, Nq, d]. Asynchronous on ``stream``;
-    lengths outside [0, Nk] are reported by :func:`solattn_get_status` on the workspace."""
+    lengths outside [0, Nk] are reported by :func:`solattn_get_status` on the workspace (without
+    one given they are cut all the same, and not reported). A workspace that the call takes itself, and
+    a new ``out``, belong to ``stream``; order other streams behind it before they use ``out``."""
     if _fast is not None:
         rc = _fast.cross(_at["solattn_cross"], q, k, v, key_len, out, workspace, stream)
         if rc is not None:

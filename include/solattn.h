@@ -376,7 +376,9 @@ int solattn_selftest_exp2(const float *x, float *y, int n, void *stream);
  *   empty rows a query that sees no key gives a row of zeros
  *   rounding   the probabilities (8-bit pages: times the value's scale) are rounded to the product's 16-bit type,
  *              bf16, or fp16 for fp16 and 8-bit pages: off by at most 2^-8 (2^-11) of their value, or in fp16 by 2^-25 of the row's
- *              largest where they are below 2^-14 of it. Sums and outputs are in 32 bits until the last rounding
+ *              largest where they are below 2^-14 of it. Sums and outputs are in 32 bits until the last rounding, with
+ *              probabilities of up to 2^15 before it: bf16 values from 2^112 up may overflow. Scales of 8-bit pages may be
+ *              negative or zero; those of values count from 2^-100 to 2^100 in magnitude
  *   masked     keys and values behind a sequence's length are not used, whatever they hold.
  *              Keys that only LATER queries see (causal) must have finite values (v)
  *   lengths    cu and len are device data and unknown to the host. Values outside the
@@ -384,7 +386,7 @@ int solattn_selftest_exp2(const float *x, float *y, int n, void *stream);
  *              dropped); either is recorded as SOLATTN_ETABLE in the workspace's status word
  *   workspace  device, 256-byte aligned, of the size that the size function gives; its first 256 bytes must be
  *              zero before its first use. The status word keeps the first error until the
- *              caller clears it. Not to be used by two calls that may run at the same time
+ *              caller clears it (the binding's calls without a workspace take one of their own, so nobody sees its status). Not to be used by two calls that may run at the same time
  *   errors     as solattn_forward; nothing is queued on an error
  * ---------------------------------------------------------------------------------------
  */
@@ -455,8 +457,9 @@ int solattn_paged_forward(const solattn_view *q, const solattn_view *out, const 
  * Writes the new tokens' keys and values [total][Hkv][d] into their pages. 8-bit kinds:
  * scale = fl(max|x| / TOP) and code = nearest(x TOP / max|x|), ties to even, TOP = 127
  * (int8) or 448 (e4m3); a row of zeros has scale 0, a row with an infinity or NaN has scale
- * NaN. Two new tokens that share a page's row (pages shared by two sequences) are written in
- * no particular order. status: device, 256-byte aligned, 256 bytes, zero before first use
+ * NaN. Where two new tokens share a page's row (pages shared by two sequences) the row's codes and scale are
+ * pieces of either, in no particular order. Lengths out of range are cut as the attention cuts them; tokens in front of
+ * their sequence's first position are not written. status: device, 256-byte aligned, 256 bytes, zero before first use
  * (any workspace of the calls above serves).
  */
 int solattn_cache_append(const solattn_cache *cache, const solattn_view *new_k, const solattn_view *new_v,
