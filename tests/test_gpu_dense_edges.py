@@ -230,6 +230,8 @@ def paged_oracle8(q, k, v, ks, vs, table, ns, lens, causal, dtype):
     bound = torch.zeros_like(o)
     t0 = 0
     for b, (n, L) in enumerate(zip(ns, lens)):
+        if n == 0:
+            continue
         kk, _, _ = du.cached(k, ks, table[b], page, L)
         vv, codes, _ = du.cached(v, vs, table[b], page, L)
         pos = torch.arange(L, device=q.device)
